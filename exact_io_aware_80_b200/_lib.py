@@ -29,6 +29,7 @@ FA_BF16 = 1
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _F = ctypes.c_float
+_L = ctypes.c_longlong
 SIGNATURES = {
     "fa_fwd": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _I, _P]),
     "fa_bwd_workspace_bytes": (ctypes.c_size_t, [_I, _I, _I]),
@@ -57,6 +58,13 @@ SIGNATURES = {
     "fa_lse_merge": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P]),
     "fa_accumulate": (_I, [_P, _P, ctypes.c_longlong, _I, _I, _P]),
     "fa_cast_f32": (_I, [_P, _P, ctypes.c_longlong, _I, _P]),
+    "fa_rotary": (_I, [_P] * 6 + [_I] * 8 + [_F] + [_L] * 5 + [_I, _P]),
+    "fa_fp8_cache_append": (_I, [_P] * 8 + [_I] * 5 + [_L] * 4 + [_I, _P]),
+    "fa_fp8_cache_read": (_I, [_P] * 7 + [_I] * 5 + [_I, _P]),
+    "fa_decode_fp8_num_splits": (_I, [_I, _I, _I, _I]),
+    "fa_decode_fp8": (_I, [_P] * 9 + [_I] * 5 + [_F, _I, _I, _P]),
+    "fa_decode_prefix_splits": (_I, [_I, _I, _I, _I, _I]),
+    "fa_decode_shared_prefix": (_I, [_P] * 11 + [_I] * 6 + [_F, _I, _I, _I, _P]),
     "fa_get_device_status": (_I, [_P]),
     "fa_watchdog_selftest": (_I, [_I, _P]),
     "fa_status_string": (ctypes.c_char_p, [_I]),
@@ -214,6 +222,48 @@ def fa_accumulate(acc, part, n, init, dt, stream):
 
 def fa_cast_f32(acc, out, n, dt, stream):
     return _check("fa_cast_f32", load().fa_cast_f32(acc, out, n, dt, stream))
+
+
+def fa_rotary(q, k, q_out, k_out, positions, turns, B, N, Hq, Hkv, d, rot_dim, interleaved, inverse, magnitude,
+              q_batch_stride, q_token_stride, k_batch_stride, k_token_stride, position_batch_stride, dt, stream):
+    return _check("fa_rotary", load().fa_rotary(q, k, q_out, k_out, positions, turns, B, N, Hq, Hkv, d, rot_dim,
+                                                int(interleaved), int(inverse), magnitude, q_batch_stride,
+                                                q_token_stride, k_batch_stride, k_token_stride,
+                                                position_batch_stride, dt, stream))
+
+
+def fa_fp8_cache_append(k, v, k8, v8, k_scale, v_scale, start, counts, B, n, Hkv, Nk_max, d, k_batch_stride,
+                        k_token_stride, v_batch_stride, v_token_stride, dt, stream):
+    return _check("fa_fp8_cache_append", load().fa_fp8_cache_append(k, v, k8, v8, k_scale, v_scale, start, counts, B,
+                                                                    n, Hkv, Nk_max, d, k_batch_stride, k_token_stride,
+                                                                    v_batch_stride, v_token_stride, dt, stream))
+
+
+def fa_fp8_cache_read(k8, v8, k_scale, v_scale, seqlens_k, k, v, B, Nk, Hkv, Nk_max, d, dt, stream):
+    return _check("fa_fp8_cache_read", load().fa_fp8_cache_read(k8, v8, k_scale, v_scale, seqlens_k, k, v, B, Nk, Hkv,
+                                                                Nk_max, d, dt, stream))
+
+
+def fa_decode_fp8_num_splits(B, Hkv, Nk_max, num_sms=0):
+    return load().fa_decode_fp8_num_splits(B, Hkv, Nk_max, num_sms)
+
+
+def fa_decode_fp8(q, k8, v8, k_scale, v_scale, seqlens_k, o, lse, workspace, B, Hq, Hkv, Nk_max, d, scale, num_splits,
+                  dt, stream):
+    return _check("fa_decode_fp8", load().fa_decode_fp8(q, k8, v8, k_scale, v_scale, seqlens_k, o, lse, workspace, B,
+                                                        Hq, Hkv, Nk_max, d, scale, num_splits, dt, stream))
+
+
+def fa_decode_prefix_splits(B, Hq, Hkv, Np, num_sms=0):
+    return load().fa_decode_prefix_splits(B, Hq, Hkv, Np, num_sms)
+
+
+def fa_decode_shared_prefix(q, k_prefix, v_prefix, k_cache, v_cache, k_scale, v_scale, seqlens_k, o, lse, workspace,
+                            B, Hq, Hkv, Np, Nk_max, d, scale, prefix_splits, num_splits, dt, stream):
+    return _check("fa_decode_shared_prefix",
+                  load().fa_decode_shared_prefix(q, k_prefix, v_prefix, k_cache, v_cache, k_scale, v_scale, seqlens_k,
+                                                 o, lse, workspace, B, Hq, Hkv, Np, Nk_max, d, scale, prefix_splits,
+                                                 num_splits, dt, stream))
 
 
 def fa_watchdog_selftest(limit_us, stream):

@@ -10,6 +10,7 @@
 
 #include "fa.h"
 #include "kernels.h"
+#include "serving.h"
 
 namespace {
 
@@ -80,6 +81,10 @@ void apply_drop(A& a, const DropParams& d) {
 }
 
 }  // namespace
+
+namespace fa {
+int* device_status_word() { return status_ptr(); }
+}  // namespace fa
 
 extern "C" {
 

@@ -1,0 +1,481 @@
+// prefix_sm100.cu -- one-token attention of a whole batch over one shared
+// prefix: the B G query rows of a KV head (G = Hq / Hkv heads of B sequences)
+// are the rows of one matrix product with the prefix's keys, so a K/V tile is
+// read once for up to 256 rows instead of once per sequence.
+//
+// Per KV head this is forward attention of B G rows over Np keys without a
+// mask, cut along the keys into splits that write normalised fp32 partials
+// (cache_decode.cu merges them with the sequences' own keys by log-sum-exp):
+//   S = Q K^T, t = s scale log2 e, p = 2^(t - m), l = sum p, O = P V / l.
+//
+// Bound by HBM up to 256 rows: 64 KB of K and V per 128-key tile against 16.8
+// MFLOP on the tensor cores and 32768 exponentials; by the tensor cores and the
+// exponentials beyond, when several row blocks read one tile from L2.
+//
+// The machinery is the forward kernel's (fwd_sm100.cu): a persistent CTA per
+// SM; one or two 128-row query tiles; one thread issuing TMA loads of K and V
+// into a two-stage ring, one issuing tcgen05 MMAs with S, P and O in TMEM, and
+// a warpgroup per query tile with one row per thread.  What differs:
+//  * a query tile packs 128 / G whole sequences: its TMA box is 64 columns x G
+//    heads x (128 / G) sequences of q [B, Hq, d], so row r is head r % G of
+//    sequence r / G.  Rows past G (128 / G), up to 127, hold whatever the
+//    shared memory held; a row's results never reach another row's;
+//  * the output is fp32, staged 32 columns at a time and written by a TMA box of
+//    the same shape into o_part [B, Hq, S, d].
+#include <cuda.h>
+#include <math.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "serving.h"
+#include "sm100.cuh"
+
+namespace fa {
+namespace {
+
+using namespace sm100;
+
+constexpr int kBM = 128;     // rows of a query tile (= TMEM lanes)
+constexpr int kBN = 128;     // keys per K/V tile
+constexpr int kStages = 2;   // K/V ring depth
+// Register split with two query tiles: launched at 168 per thread (384 x 168 = 64512), the
+// load/MMA warpgroup drops to 104 and the softmax warpgroups rise to 200 (2 x 128 x 200 +
+// 128 x 104 = 64512).  One query tile (256 threads) needs no split.
+constexpr int kRegsSoftmax = 200;
+constexpr int kRegsControl = 104;
+constexpr float kRescaleThreshold = 8.0f;  // log2 units: rescale O when m grows by more than 2^8
+
+template <int D, int NT>
+struct Smem {
+  static constexpr int kPanel = 128 * 128;  // one [128 rows][128 bytes] swizzled panel
+  static constexpr int kTile = (D / 64) * kPanel;
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffK = kOffQ + NT * kTile;
+  static constexpr int kOffV = kOffK + kStages * kTile;
+  static constexpr int kOffStage = kOffV + kStages * kTile;  // 32 fp32 columns per query tile
+  static constexpr int kOffBar = kOffStage + NT * kPanel;
+  enum { kBarQ = 0, kBarKFull = 1, kBarKEmpty = 3, kBarVFull = 5, kBarVEmpty = 7, kBarS = 9, kBarP = 11, kBarO = 13,
+         kBarDrain = 15, kBarQEmpty = 16, kBarOFree = 17, kBarStageFull = 19, kBarStageDone = 21, kNumBars = 23 };
+  static constexpr int kOffTmem = kOffBar + kNumBars * 8;
+  static constexpr int kOffAbort = kOffTmem + 4;
+  static constexpr int kBytes = kOffAbort + 4 + 1024;  // + slack to align the base to 1024 B
+  static_assert(kBytes <= 232448, "shared memory per CTA exceeded");
+  static constexpr int kThreads = 128 * (NT + 1);
+  // TMEM columns: S_t, then O_t
+  static constexpr uint32_t col_s(int t) { return 128u * t; }
+  static constexpr uint32_t col_o(int t) { return 128u * NT + 128u * t; }
+  static constexpr uint32_t kCols = 256u * NT;
+};
+
+struct Params {
+  float* lse_part;  // [B,Hq,S]
+  int B, Hq, Hkv, Np, G, seqs;  // seqs = 128 / G sequences per query tile
+  int S;                        // splits per row of the partials (prefix and cache)
+  int splits, chunk;            // prefix splits and their keys
+  int row_blocks;               // NT query tiles each
+  int num_work;                 // splits * Hkv * row_blocks
+  float scale_log2;
+  int* status;
+};
+
+// Work w: row blocks of one (split, KV head) are neighbours, so the CTAs that share its K/V tiles
+// run together.
+struct Work {
+  int rb, hk, s;
+};
+__device__ __forceinline__ Work work_at(const Params& p, int w) {
+  return Work{w % p.row_blocks, (w / p.row_blocks) % p.Hkv, w / (p.row_blocks * p.Hkv)};
+}
+
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(Smem<D, NT>::kThreads, 1)
+    prefix_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                        const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO, Params p) {
+  using L = Smem<D, NT>;
+  constexpr int kWarpLoad = 4 * NT, kWarpMma = 4 * NT + 1;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t sb = (raw + 1023u) & ~1023u;
+  uint8_t* gb = smem_raw + (sb - raw);
+  auto bar = [&](int i) { return sb + L::kOffBar + 8u * i; };
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(gb + L::kOffAbort);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // the cache's partials, launched next as a programmatic dependent, share no memory with this
+  // kernel's and may fill SMs as its CTAs leave
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  auto blocks_of = [&](const Work& x) {  // K/V tiles of a split
+    return (min(p.chunk, p.Np - x.s * p.chunk) + kBN - 1) / kBN;
+  };
+
+  if (tid == 0) {
+    for (int i = 0; i < L::kNumBars; ++i)
+      mbar_init(bar(i), (i == L::kBarP || i == L::kBarP + 1 || i == L::kBarOFree || i == L::kBarOFree + 1 ||
+                         i == L::kBarStageFull || i == L::kBarStageFull + 1)
+                            ? kBM
+                            : 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == kWarpMma) {
+    tmem_alloc(sb + L::kOffTmem, L::kCols);
+    tmem_relinquish();
+  }
+  if (warp == kWarpLoad && lane == 0) {
+    prefetch_tmap(&tmQ);
+    prefetch_tmap(&tmK);
+    prefetch_tmap(&tmV);
+    prefetch_tmap(&tmO);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = *reinterpret_cast<volatile uint32_t*>(gb + L::kOffTmem);
+
+  if (warp >= kWarpLoad) {
+   if constexpr (NT == 2) regs_decrease<kRegsControl>();
+   if (warp == kWarpLoad) {
+    // ------------------------------------------------------------------ TMA producer
+    if (lane == 0) {
+      const uint32_t q_bytes = (uint32_t)(p.G * p.seqs * 128 * (D / 64));  // of one query tile's boxes
+      int last_k[kStages] = {-1, -1}, last_v[kStages] = {-1, -1};
+      int last_q = -1;
+      int g = 0;  // K/V tiles loaded so far by this CTA (ring position)
+      int wl = 0;
+      for (int w = blockIdx.x; w < p.num_work; w += gridDim.x, ++wl) {
+        const Work x = work_at(p, w);
+        const int nblk = blocks_of(x), key0 = x.s * p.chunk;
+        // the previous work's last score MMAs must have read Q before it is replaced
+        if (wl > 0 && !mbar_wait(bar(L::kBarQEmpty), (wl - 1) & 1, abort_flag, p.status)) break;
+        mbar_expect_tx(bar(L::kBarQ), NT * q_bytes);
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int pn = 0; pn < D / 64; ++pn)
+            tma_load_4d(sb + L::kOffQ + t * L::kTile + pn * L::kPanel, &tmQ, bar(L::kBarQ), 64 * pn, x.hk * p.G,
+                        (x.rb * NT + t) * p.seqs, 0);
+        last_q = wl;
+        bool stop = false;
+        for (int j = 0; j < nblk; ++j, ++g) {
+          const int st = g & 1, u = g >> 1;
+          if (u > 0 && !mbar_wait(bar(L::kBarKEmpty + st), (u - 1) & 1, abort_flag, p.status)) {
+            stop = true;
+            break;
+          }
+          mbar_expect_tx(bar(L::kBarKFull + st), L::kTile);
+#pragma unroll
+          for (int pn = 0; pn < D / 64; ++pn)
+            tma_load_4d(sb + L::kOffK + st * L::kTile + pn * L::kPanel, &tmK, bar(L::kBarKFull + st), 64 * pn, x.hk,
+                        key0 + j * kBN, 0);
+          last_k[st] = u;
+          if (u > 0 && !mbar_wait(bar(L::kBarVEmpty + st), (u - 1) & 1, abort_flag, p.status)) {
+            stop = true;
+            break;
+          }
+          mbar_expect_tx(bar(L::kBarVFull + st), L::kTile);
+#pragma unroll
+          for (int pn = 0; pn < D / 64; ++pn)
+            tma_load_4d(sb + L::kOffV + st * L::kTile + pn * L::kPanel, &tmV, bar(L::kBarVFull + st), 64 * pn, x.hk,
+                        key0 + j * kBN, 0);
+          last_v[st] = u;
+        }
+        if (stop) break;
+      }
+      if (*abort_flag) {
+        // let every copy this thread issued land before the CTA releases its shared memory
+        if (last_q >= 0) wait_drain(bar(L::kBarQ), last_q & 1, p.status);
+        for (int st = 0; st < kStages; ++st) {
+          if (last_k[st] >= 0) wait_drain(bar(L::kBarKFull + st), last_k[st] & 1, p.status);
+          if (last_v[st] >= 0) wait_drain(bar(L::kBarVFull + st), last_v[st] & 1, p.status);
+        }
+      }
+    }
+  } else if (warp == kWarpMma) {
+    // ------------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      constexpr bool kBf16 = Elem<T>::kBf16;
+      constexpr uint32_t idq = idesc_f16(kBf16, kBM, kBN, false);
+      constexpr uint32_t idv = idesc_f16(kBf16, kBM, D, true);
+      auto qk = [&](int t, int st) {
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t ko = (kk >> 2) * L::kPanel + (kk & 3) * 32;
+          const uint64_t a = sdesc_sw128(sb + L::kOffQ + t * L::kTile + ko, 16, 1024);
+          const uint64_t bd = sdesc_sw128(sb + L::kOffK + st * L::kTile + ko, 16, 1024);
+          mma_ss(tbase + L::col_s(t), a, bd, idq, kk > 0 ? 1u : 0u);
+        }
+      };
+      auto pv = [&](int t, int st, bool first) {
+#pragma unroll
+        for (int kk = 0; kk < kBN / 16; ++kk) {
+          // V stored [keys][d]: B is N(=d)-major; 16 keys = two 8-row groups of 128 B
+          const uint64_t bd = sdesc_sw128(sb + L::kOffV + st * L::kTile + kk * 2048, L::kPanel, 1024);
+          mma_ts(tbase + L::col_o(t), tbase + L::col_s(t) + kk * 8, bd, idv, (!first || kk > 0) ? 1u : 0u);
+        }
+      };
+      bool ok = true;
+      int g = 0;  // K/V tiles consumed so far by this CTA; S/P barriers complete once per tile
+      int wl = 0;
+      for (int w = blockIdx.x; ok && w < p.num_work; w += gridDim.x, ++wl) {
+        const int nblk = blocks_of(work_at(p, w));
+        ok = mbar_wait(bar(L::kBarQ), wl & 1, abort_flag, p.status) &&
+             mbar_wait(bar(L::kBarKFull + (g & 1)), (g >> 1) & 1, abort_flag, p.status);
+        if (!ok) break;
+        tc_fence_after();
+        // the previous work's last PV ran before these in issue order; its S/P buffers are free
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          qk(t, g & 1);
+          mma_commit(bar(L::kBarS + t));
+        }
+        mma_commit(bar(L::kBarKEmpty + (g & 1)));
+        if (nblk == 1) mma_commit(bar(L::kBarQEmpty));
+        for (int j = 0; ok && j < nblk; ++j, ++g) {
+          const int st = g & 1, u = g >> 1;
+          const bool more = j + 1 < nblk;
+          const int st1 = (g + 1) & 1, u1 = (g + 1) >> 1;
+          ok = mbar_wait(bar(L::kBarVFull + st), u & 1, abort_flag, p.status);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            ok = ok && mbar_wait(bar(L::kBarP + t), g & 1, abort_flag, p.status);
+            // the first PV of a work overwrites O_t: the previous epilogue must have read it
+            if (ok && j == 0 && wl > 0) ok = mbar_wait(bar(L::kBarOFree + t), (wl - 1) & 1, abort_flag, p.status);
+            if (!ok) break;
+            tc_fence_after();
+            pv(t, st, j == 0);
+            if (!more) mma_commit(bar(L::kBarO + t));
+            if (more) {
+              if (t == 0) {
+                ok = mbar_wait(bar(L::kBarKFull + st1), u1 & 1, abort_flag, p.status);
+                if (!ok) break;
+                tc_fence_after();
+              }
+              qk(t, st1);  // overwrites S_t / P_t after PV in issue order
+              mma_commit(bar(L::kBarS + t));
+            }
+          }
+          if (!ok) break;
+          if (!more) mma_commit(bar(L::kBarVEmpty + st));  // inside a work the softmax warps free V (below)
+          if (more && j + 2 == nblk) mma_commit(bar(L::kBarQEmpty));  // last score MMAs issued
+        }
+      }
+      // no MMA may still run when TMEM is released
+      mma_commit(bar(L::kBarDrain));
+      wait_drain(bar(L::kBarDrain), 0, p.status);
+    }
+   }
+  } else {
+    if constexpr (NT == 2) regs_increase<kRegsSoftmax>();
+    // ------------------------------------------------------------------ softmax + epilogue
+    const int t = warp >> 2;
+    const int wq = warp & 3;
+    const int rr = wq * 32 + lane;  // row of the query tile
+    const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
+    const uint32_t tS = tbase + lane_off + L::col_s(t);
+    const uint32_t tO = tbase + lane_off + L::col_o(t);
+    const float c = p.scale_log2;
+    bool ok = true;
+    int g = 0;  // K/V tiles processed so far by this CTA
+    int wl = 0;
+    for (int w = blockIdx.x; ok && w < p.num_work; w += gridDim.x, ++wl) {
+      const Work x = work_at(p, w);
+      const int nblk = blocks_of(x), key0 = x.s * p.chunk;
+      float m_ref = -INFINITY, l = 0.f;
+      for (int j = 0; j < nblk; ++j, ++g) {
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarS + t), g & 1, abort_flag, p.status));
+        if (!ok) break;
+        if (t == NT - 1 && wq == 0 && lane == 0 && j != 0) {
+          // the last tile's S of tile g is complete, and with it every MMA issued before it: the
+          // score MMAs of tile g (its K stage is free) and the PV of tile g - 1 (its V stage is)
+          mbar_arrive(bar(L::kBarKEmpty + (g & 1)));
+          mbar_arrive(bar(L::kBarVEmpty + ((g - 1) & 1)));
+        }
+        tc_fence_after();
+        float s[kBN];
+        {
+          uint32_t r0[32], r1[32], r2[32], r3[32];
+          tmem_ld32(tS + 0, r0);
+          tmem_ld32(tS + 32, r1);
+          tmem_ld32(tS + 64, r2);
+          tmem_ld32(tS + 96, r3);
+          tmem_wait_ld();
+          reg_fence(r0);
+          reg_fence(r1);
+          reg_fence(r2);
+          reg_fence(r3);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            s[i] = __uint_as_float(r0[i]);
+            s[32 + i] = __uint_as_float(r1[i]);
+            s[64 + i] = __uint_as_float(r2[i]);
+            s[96 + i] = __uint_as_float(r3[i]);
+          }
+        }
+        const int lim = p.Np - (key0 + j * kBN);  // keys of this tile inside the prefix
+        if (lim < kBN) {
+#pragma unroll
+          for (int i = 0; i < kBN; ++i)
+            if (i >= lim) s[i] = -INFINITY;
+        }
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int i = 0; i < kBN; i += 8) {
+          mx[0] = max3(mx[0], s[i], s[i + 1]);
+          mx[1] = max3(mx[1], s[i + 2], s[i + 3]);
+          mx[2] = max3(mx[2], s[i + 4], s[i + 5]);
+          mx[3] = max3(mx[3], s[i + 6], s[i + 7]);
+        }
+        const float mxs = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+        const bool resc = mxs > m_ref + kRescaleThreshold;
+        const float corr = resc ? ex2(m_ref - mxs) : 1.f;
+        if (resc) m_ref = mxs;
+        l *= corr;
+        const float mu = (m_ref == -INFINITY) ? 0.f : m_ref;
+        const float2 c2 = make_float2(c, c), nm2 = make_float2(-mu, -mu);
+        float2 rs0 = make_float2(0.f, 0.f), rs1 = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            const int c0 = 64 * half + 2 * i;
+            const float2 xa = __ffma2_rn(make_float2(s[c0], s[c0 + 1]), c2, nm2);
+            const float2 xb = __ffma2_rn(make_float2(s[c0 + 2], s[c0 + 3]), c2, nm2);
+            const float2 a = make_float2(ex2(xa.x), ex2(xa.y)), bb = make_float2(ex2(xb.x), ex2(xb.y));
+            rs0 = __fadd2_rn(rs0, a);
+            rs1 = __fadd2_rn(rs1, bb);
+            pk[i] = Elem<T>::pack(a.x, a.y);
+            pk[i + 1] = Elem<T>::pack(bb.x, bb.y);
+          }
+          tmem_st32(tS + 32 * half, pk);
+        }
+        l += (rs0.x + rs0.y) + (rs1.x + rs1.y);
+        if (__any_sync(0xffffffffu, resc && j > 0)) {
+#pragma unroll
+          for (int q = 0; q < D / 32; ++q) {
+            uint32_t r[32];
+            tmem_ld32(tO + q * 32, r);
+            tmem_wait_ld();
+            reg_fence(r);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * corr);
+            tmem_st32(tO + q * 32, r);
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(bar(L::kBarP + t));
+      }
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarO + t), wl & 1, abort_flag, p.status));
+      if (!ok) break;
+      uint32_t r[D];
+      // O_t: TMEM -> registers, then hand the TMEM columns back to the MMA thread at once
+      tc_fence_after();
+#pragma unroll
+      for (int q = 0; q < D / 32; ++q) tmem_ld32(tO + q * 32, *reinterpret_cast<uint32_t(*)[32]>(r + 32 * q));
+      tmem_wait_ld();
+#pragma unroll
+      for (int q = 0; q < D / 32; ++q) reg_fence(*reinterpret_cast<uint32_t(*)[32]>(r + 32 * q));
+      tc_fence_before();
+      mbar_arrive(bar(L::kBarOFree + t));
+
+      const int b0 = (x.rb * NT + t) * p.seqs;  // first sequence of this query tile
+      const float inv = l == 0.f ? 0.f : 1.f / l;  // every score -inf: O = 0, LSE = -inf
+      const int b = b0 + rr / p.G;
+      if (rr < p.G * p.seqs && b < p.B) {
+        const long li = ((long)b * p.Hq + x.hk * p.G + rr % p.G) * p.S + x.s;
+        if (FA_IN_BOUNDS(p.status, li, (long)p.B * p.Hq * p.S))
+          p.lse_part[li] = ((m_ref == -INFINITY ? 0.f : m_ref) + log2f(l)) * kLn2;
+      }
+      const uint32_t half = sb + L::kOffStage + t * L::kPanel;
+#pragma unroll
+      for (int pn = 0; pn < D / 32; ++pn) {
+        const int u = wl * (D / 32) + pn;  // uses of this tile's stage so far
+        if (u > 0)
+          ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarStageDone + t), (u - 1) & 1, abort_flag, p.status));
+        if (!ok) break;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          auto f = [&](int i) { return __float_as_uint(__uint_as_float(r[32 * pn + 4 * k + i]) * inv); };
+          st_shared_v4(half + rr * 128 + ((k ^ (rr & 7)) << 4), f(0), f(1), f(2), f(3));
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(bar(L::kBarStageFull + t));
+        if (wq == 0 && lane == 0) {
+          ok = mbar_wait(bar(L::kBarStageFull + t), u & 1, abort_flag, p.status);
+          if (ok) {
+            if (b0 < p.B) {  // a block's second tile may hold no sequence
+              tma_store_4d(&tmO, half, 32 * pn, x.s, x.hk * p.G, b0);
+              bulk_commit();
+              bulk_wait_read_all();
+            }
+            mbar_arrive(bar(L::kBarStageDone + t));
+          }
+        }
+        ok = __all_sync(0xffffffffu, ok);
+      }
+    }
+    // stores must be complete before the CTA exits
+    if (wq == 0 && lane == 0) bulk_wait_all();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kWarpMma) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tbase, L::kCols);
+  }
+}
+
+template <typename T, int D, int NT>
+cudaError_t launch(const CacheDecodeArgs& a, cudaStream_t s) {
+  const int G = a.Hq / a.Hkv, seqs = kBM / G, S = a.prefix_splits + a.num_splits;
+  const int type = Elem<T>::kBf16 ? kMapBf16 : kMapF16;
+  CUtensorMap mq, mk, mv, mo;
+  {
+    const uint64_t dims[4] = {D, (uint64_t)a.Hq, (uint64_t)a.B, 1};
+    const uint64_t st[3] = {D * 2, (uint64_t)a.Hq * D * 2, (uint64_t)a.B * a.Hq * D * 2};
+    const uint32_t box[4] = {64, (uint32_t)G, (uint32_t)seqs, 1};
+    if (!make_map_box(&mq, a.q, type, dims, st, box)) return cudaErrorInvalidValue;
+  }
+  {
+    const uint64_t dims[4] = {D, (uint64_t)S, (uint64_t)a.Hq, (uint64_t)a.B};
+    const uint64_t st[3] = {D * 4, (uint64_t)S * D * 4, (uint64_t)a.Hq * S * D * 4};
+    const uint32_t box[4] = {32, 1, (uint32_t)G, (uint32_t)seqs};
+    if (!make_map_box(&mo, a.o_part, kMapF32, dims, st, box)) return cudaErrorInvalidValue;
+  }
+  if (!make_map(&mk, a.kp, Elem<T>::kBf16, D, a.Hkv, a.Np, 1, kBN) ||
+      !make_map(&mv, a.vp, Elem<T>::kBf16, D, a.Hkv, a.Np, 1, kBN))
+    return cudaErrorInvalidValue;
+  const int rows = (a.B + NT * seqs - 1) / (NT * seqs);
+  const long long work = (long long)rows * a.Hkv * a.prefix_splits;
+  if (work > (1ll << 30)) return cudaErrorInvalidValue;
+  Params p{a.lse_part, a.B, a.Hq, a.Hkv, a.Np, G, seqs, S, a.prefix_splits, a.prefix_chunk, rows, (int)work,
+           a.scale * kLog2e, a.status};
+  auto kern = prefix_sm100_kernel<T, D, NT>;
+  constexpr int smem = Smem<D, NT>::kBytes;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const int grid = (int)std::min<long long>(work, device_sm_count());
+  kern<<<grid, Smem<D, NT>::kThreads, smem, s>>>(mq, mk, mv, mo, p);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_t(const CacheDecodeArgs& a, cudaStream_t s) {
+  const bool one = (long)a.B <= kBM / (a.Hq / a.Hkv);  // every sequence fits one query tile
+  if (a.d == 128) return one ? launch<T, 128, 1>(a, s) : launch<T, 128, 2>(a, s);
+  return one ? launch<T, 64, 1>(a, s) : launch<T, 64, 2>(a, s);
+}
+
+}  // namespace
+
+cudaError_t launch_prefix_sm100(const CacheDecodeArgs& a, cudaStream_t s) {
+  return a.bf16 ? launch_t<__nv_bfloat16>(a, s) : launch_t<__half>(a, s);
+}
+
+}  // namespace fa

@@ -1,0 +1,80 @@
+// serving.h -- host-side launchers of the rotary, E4M3-cache and cache-decode
+// kernels (internal to libfa.so).  Arguments are validated in serving_api.cu
+// before any launcher runs.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace fa {
+
+// Device status word of the current device (fa_api.cu), nullptr if it cannot be found.
+int* device_status_word();
+
+// 4-D tensor map with 128-byte swizzle (tma.cu): dims innermost first, strides of dims 1..3 in
+// bytes; the box's innermost extent must be 128 bytes.
+constexpr int kMapF16 = 0, kMapBf16 = 1, kMapF32 = 2;
+bool make_map_box(CUtensorMap* m, const void* base, int type, const uint64_t dims[4], const uint64_t strides[3],
+                  const uint32_t box[4]);
+
+// Rotary positions of q [B,N,Hq,d] and k [B,N,Hkv,d] (rotary.cu).  Input strides in elements
+// (heads are d apart); outputs contiguous, or the inputs themselves.
+struct RotaryArgs {
+  const void *q, *k;
+  void *q_out, *k_out;
+  const int* positions;  // [B,N] (pos_stride = N) or [N] (pos_stride = 0)
+  const unsigned long long* turns;  // [rot / 2]: turns per position, in units of 2^-64 turn
+  int B, N, Hq, Hkv, d, rot;
+  long q_bs, q_ts, k_bs, k_ts;  // batch and token strides of q and k
+  long pos_stride;
+  int interleaved, inverse;
+  float magnitude;
+  int bf16;
+  int* status;
+};
+cudaError_t launch_rotary(const RotaryArgs& a, cudaStream_t s);
+
+// Rows of an E4M3 cache (fp8_cache.cu): codes [B,Nk_max,Hkv,d], scales [B,Hkv,Nk_max].
+struct Fp8CacheArgs {
+  const void *k, *v;  // append: [B,n,Hkv,d] 16-bit, batch and token strides below
+  long k_bs, k_ts, v_bs, v_ts;
+  uint8_t *k8, *v8;
+  float *k_scale, *v_scale;
+  const int* start;   // append: first cache row of each sequence
+  const int* counts;  // append: rows of each sequence (nullptr: n); read: live rows
+  void *k_out, *v_out;  // read: [B,n,Hkv,d] 16-bit
+  int B, n, Hkv, Nk_max, d;
+  int bf16;
+  int* status;
+};
+cudaError_t launch_fp8_cache_append(const Fp8CacheArgs& a, cudaStream_t s);
+cudaError_t launch_fp8_cache_read(const Fp8CacheArgs& a, cudaStream_t s);
+
+// One-token attention over a cache (cache_decode.cu) and over a prefix that the whole batch
+// shares (prefix_sm100.cu), both writing normalised partials that one kernel merges:
+// o_part [B,Hq,S,d] and lse_part [B,Hq,S] fp32, S = prefix_splits + num_splits, the prefix's
+// splits first.  A sequence's splits past its length are neither written nor read.
+struct CacheDecodeArgs {
+  const void* q;  // [B,1,Hq,d]
+  const void *kp, *vp;  // prefix [Np,Hkv,d] (prefix_splits > 0)
+  const void *k, *v;    // cache [B,Nk_max,Hkv,d]: 16-bit, or E4M3 codes with scales [B,Hkv,Nk_max]
+  const float *k_scale, *v_scale;
+  const int* seqlens;
+  float *o_part, *lse_part;
+  void* o;
+  float* lse;
+  int B, Hq, Hkv, Np, Nk_max, d;
+  int prefix_splits, prefix_chunk;  // keys per prefix split, a multiple of 128
+  int num_splits, chunk;            // keys per cache split, a multiple of 64
+  float scale;
+  int bf16;
+  int* status;
+};
+cudaError_t launch_prefix_sm100(const CacheDecodeArgs& a, cudaStream_t s);
+// The cache's partials; `after_prefix`: the previous launch on the stream is launch_prefix_sm100.
+cudaError_t launch_cache_decode(const CacheDecodeArgs& a, int after_prefix, cudaStream_t s);
+// The merge; always launched right after launch_cache_decode, on the same stream.
+cudaError_t launch_cache_combine(const CacheDecodeArgs& a, cudaStream_t s);
+
+}  // namespace fa

@@ -1,0 +1,292 @@
+// serving_api.cu -- C ABI of the rotary, E4M3-cache and cache-decode operators
+// (declared in include/fa.h): argument validation, split heuristics and
+// dispatch.  Validation happens before anything is launched; the library
+// allocates no device memory.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "fa.h"
+#include "kernels.h"
+#include "serving.h"
+
+namespace {
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+fa_status from_cuda(cudaError_t e) { return e == cudaSuccess ? FA_OK : FA_ERR_CUDA; }
+
+// Half-open byte range of a strided [B, N, H, d] 16-bit tensor.
+struct Range {
+  uintptr_t lo, hi;
+};
+Range range_of(const void* p, long long bs, long long ts, int B, int N, int H, int d) {
+  const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+  return Range{lo, lo + 2ull * ((unsigned long long)(B - 1) * bs + (unsigned long long)(N - 1) * ts + (unsigned long long)H * d)};
+}
+bool overlap(const Range& a, const Range& b) { return a.lo < b.hi && b.lo < a.hi; }
+
+// Element strides of the token and batch dimensions: whole 16-byte chunks, and far below the
+// point where an address computation could leave 64 bits.
+bool strides_ok(long long bs, long long ts) {
+  const long long most = 1ll << 40;
+  return bs >= 0 && ts >= 0 && bs <= most && ts <= most;
+}
+bool strides_aligned(long long bs, long long ts) { return bs % 8 == 0 && ts % 8 == 0; }
+
+int sm_count(int num_sms) { return num_sms > 0 ? num_sms : fa::device_sm_count(); }
+
+fa_status check_decode(int B, int Hq, int Hkv, int Nk_max, int d, float scale, int num_splits, fa_dtype dt) {
+  if (B < 1 || Hq < 1 || Hkv < 1 || Nk_max < 1 || num_splits < 1) return FA_ERR_INVALID;
+  if (Hq % Hkv != 0) return FA_ERR_INVALID;
+  if (!(scale >= 0.f) || std::isinf(scale)) return FA_ERR_INVALID;
+  if (dt != FA_FP16 && dt != FA_BF16) return FA_ERR_UNSUPPORTED;
+  if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+  if (Hq / Hkv > 16) return FA_ERR_UNSUPPORTED;  // one CTA holds a GQA group of at most 16 query heads
+  if (B > 65535 || Hkv > 65535 || Hq > 65535 || num_splits > 65535) return FA_ERR_UNSUPPORTED;
+  if (Nk_max > (1 << 30)) return FA_ERR_UNSUPPORTED;
+  if (num_splits > (Nk_max + 63) / 64) return FA_ERR_INVALID;
+  return FA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+fa_status fa_rotary(const void* q, const void* k, void* q_out, void* k_out, const int* positions,
+                    const unsigned long long* turns, int B, int N, int Hq, int Hkv, int d, int rot_dim,
+                    int interleaved, int inverse, float magnitude, long long q_batch_stride, long long q_token_stride,
+                    long long k_batch_stride, long long k_token_stride, long long position_batch_stride, fa_dtype dt,
+                    fa_stream_t stream) {
+  if (!q || !q_out || !positions || !turns || (Hkv > 0 && (!k || !k_out))) return FA_ERR_INVALID;
+  if (B < 1 || N < 1 || Hq < 1 || Hkv < 0) return FA_ERR_INVALID;
+  if (rot_dim < 2 || rot_dim > d) return FA_ERR_INVALID;
+  if (!std::isfinite(magnitude)) return FA_ERR_INVALID;
+  if (position_batch_stride != 0 && position_batch_stride < N) return FA_ERR_INVALID;
+  if (!strides_ok(q_batch_stride, q_token_stride) || (Hkv > 0 && !strides_ok(k_batch_stride, k_token_stride)))
+    return FA_ERR_INVALID;
+  if (dt != FA_FP16 && dt != FA_BF16) return FA_ERR_UNSUPPORTED;
+  if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+  if (rot_dim % 16 != 0) return FA_ERR_UNSUPPORTED;
+  if (B > 65535 || Hq > 65535 || Hkv > 65535) return FA_ERR_UNSUPPORTED;
+  if ((long long)B * N > (1ll << 31) - 1) return FA_ERR_UNSUPPORTED;
+  if (!aligned(q, 16) || !aligned(q_out, 16) || !aligned(positions, 4) || !aligned(turns, 8) ||
+      !strides_aligned(q_batch_stride, q_token_stride))
+    return FA_ERR_ALIGN;
+  if (Hkv > 0 && (!aligned(k, 16) || !aligned(k_out, 16) || !strides_aligned(k_batch_stride, k_token_stride)))
+    return FA_ERR_ALIGN;
+  // an output is its own input, element for element, or apart from both inputs and the other output
+  const long long qt = (long long)Hq * d, kt = (long long)Hkv * d;
+  const Range qi = range_of(q, q_batch_stride, q_token_stride, B, N, Hq, d), qo = range_of(q_out, N * qt, qt, B, N, Hq, d);
+  if (q_out == q ? !((N == 1 || q_token_stride == qt) && (B == 1 || q_batch_stride == N * qt)) : overlap(qo, qi))
+    return FA_ERR_INVALID;
+  if (Hkv > 0) {
+    const Range ki = range_of(k, k_batch_stride, k_token_stride, B, N, Hkv, d), ko = range_of(k_out, N * kt, kt, B, N, Hkv, d);
+    if (k_out == k ? !((N == 1 || k_token_stride == kt) && (B == 1 || k_batch_stride == N * kt)) : overlap(ko, ki))
+      return FA_ERR_INVALID;
+    if (overlap(qo, ko) || overlap(qo, ki) || overlap(ko, qi)) return FA_ERR_INVALID;
+  }
+  fa::RotaryArgs a{q, k, q_out, k_out, positions, turns, B, N, Hq, Hkv, d, rot_dim, q_batch_stride, q_token_stride,
+                   k_batch_stride, k_token_stride, position_batch_stride, interleaved ? 1 : 0, inverse ? 1 : 0,
+                   magnitude, dt == FA_BF16 ? 1 : 0, fa::device_status_word()};
+  if (!a.status) return FA_ERR_CUDA;
+  return from_cuda(fa::launch_rotary(a, static_cast<cudaStream_t>(stream)));
+}
+
+fa_status fa_fp8_cache_append(const void* k, const void* v, void* k8, void* v8, float* k_scale, float* v_scale,
+                              const int* start, const int* counts, int B, int n, int Hkv, int Nk_max, int d,
+                              long long k_batch_stride, long long k_token_stride, long long v_batch_stride,
+                              long long v_token_stride, fa_dtype dt, fa_stream_t stream) {
+  if (!k || !v || !k8 || !v8 || !k_scale || !v_scale || !start) return FA_ERR_INVALID;
+  if (B < 1 || n < 1 || Hkv < 1 || Nk_max < 1) return FA_ERR_INVALID;
+  if (!strides_ok(k_batch_stride, k_token_stride) || !strides_ok(v_batch_stride, v_token_stride)) return FA_ERR_INVALID;
+  if (dt != FA_FP16 && dt != FA_BF16) return FA_ERR_UNSUPPORTED;
+  if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+  if (B > 65535 || Hkv > 65535 || Nk_max > (1 << 30)) return FA_ERR_UNSUPPORTED;
+  if ((long long)B * n > (1ll << 31) - 1) return FA_ERR_UNSUPPORTED;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(k8, 16) || !aligned(v8, 16) || !aligned(k_scale, 4) ||
+      !aligned(v_scale, 4) || !aligned(start, 4) || (counts && !aligned(counts, 4)) ||
+      !strides_aligned(k_batch_stride, k_token_stride) || !strides_aligned(v_batch_stride, v_token_stride))
+    return FA_ERR_ALIGN;
+  fa::Fp8CacheArgs a{};
+  a.k = k;
+  a.v = v;
+  a.k_bs = k_batch_stride;
+  a.k_ts = k_token_stride;
+  a.v_bs = v_batch_stride;
+  a.v_ts = v_token_stride;
+  a.k8 = static_cast<uint8_t*>(k8);
+  a.v8 = static_cast<uint8_t*>(v8);
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.start = start;
+  a.counts = counts;
+  a.B = B;
+  a.n = n;
+  a.Hkv = Hkv;
+  a.Nk_max = Nk_max;
+  a.d = d;
+  a.bf16 = dt == FA_BF16 ? 1 : 0;
+  a.status = fa::device_status_word();
+  if (!a.status) return FA_ERR_CUDA;
+  return from_cuda(fa::launch_fp8_cache_append(a, static_cast<cudaStream_t>(stream)));
+}
+
+fa_status fa_fp8_cache_read(const void* k8, const void* v8, const float* k_scale, const float* v_scale,
+                            const int* seqlens_k, void* k, void* v, int B, int Nk, int Hkv, int Nk_max, int d,
+                            fa_dtype dt, fa_stream_t stream) {
+  if (!k8 || !v8 || !k_scale || !v_scale || !seqlens_k || !k || !v) return FA_ERR_INVALID;
+  if (B < 1 || Nk < 1 || Hkv < 1 || Nk_max < Nk) return FA_ERR_INVALID;
+  if (dt != FA_FP16 && dt != FA_BF16) return FA_ERR_UNSUPPORTED;
+  if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+  if (B > 65535 || Hkv > 65535 || Nk_max > (1 << 30)) return FA_ERR_UNSUPPORTED;
+  if ((long long)B * Nk > (1ll << 31) - 1) return FA_ERR_UNSUPPORTED;
+  if (!aligned(k8, 16) || !aligned(v8, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(k_scale, 4) ||
+      !aligned(v_scale, 4) || !aligned(seqlens_k, 4))
+    return FA_ERR_ALIGN;
+  fa::Fp8CacheArgs a{};
+  a.k8 = static_cast<uint8_t*>(const_cast<void*>(k8));
+  a.v8 = static_cast<uint8_t*>(const_cast<void*>(v8));
+  a.k_scale = const_cast<float*>(k_scale);
+  a.v_scale = const_cast<float*>(v_scale);
+  a.counts = seqlens_k;
+  a.k_out = k;
+  a.v_out = v;
+  a.B = B;
+  a.n = Nk;
+  a.Hkv = Hkv;
+  a.Nk_max = Nk_max;
+  a.d = d;
+  a.bf16 = dt == FA_BF16 ? 1 : 0;
+  a.status = fa::device_status_word();
+  if (!a.status) return FA_ERR_CUDA;
+  return from_cuda(fa::launch_fp8_cache_read(a, static_cast<cudaStream_t>(stream)));
+}
+
+int fa_decode_fp8_num_splits(int B, int Hkv, int Nk_max, int num_sms) {
+  if (B < 1 || Hkv < 1 || Nk_max < 1) return 1;
+  const long long units = (long long)B * Hkv;
+  const long long want = std::max<long long>(1, (26ll * sm_count(num_sms) + units - 1) / units);
+  const int cap = (Nk_max + 255) / 256;
+  const int splits = (int)std::min<long long>(want, cap);
+  const int chunk = fa_decode_chunk(Nk_max, splits);
+  return (Nk_max + chunk - 1) / chunk;
+}
+
+fa_status fa_decode_fp8(const void* q, const void* k8, const void* v8, const float* k_scale, const float* v_scale,
+                        const int* seqlens_k, void* o, float* lse, void* workspace, int B, int Hq, int Hkv, int Nk_max,
+                        int d, float scale, int num_splits, fa_dtype dt, fa_stream_t stream) {
+  if (!q || !k8 || !v8 || !k_scale || !v_scale || !seqlens_k || !o || !lse || !workspace) return FA_ERR_INVALID;
+  const fa_status st = check_decode(B, Hq, Hkv, Nk_max, d, scale, num_splits, dt);
+  if (st != FA_OK) return st;
+  if (!aligned(q, 16) || !aligned(k8, 16) || !aligned(v8, 16) || !aligned(o, 16) || !aligned(workspace, 16) ||
+      !aligned(k_scale, 4) || !aligned(v_scale, 4) || !aligned(seqlens_k, 4) || !aligned(lse, 4))
+    return FA_ERR_ALIGN;
+  fa::CacheDecodeArgs a{};
+  a.q = q;
+  a.k = k8;
+  a.v = v8;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.seqlens = seqlens_k;
+  a.o_part = static_cast<float*>(workspace);
+  a.lse_part = a.o_part + (size_t)B * Hq * num_splits * d;
+  a.o = o;
+  a.lse = lse;
+  a.B = B;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.Nk_max = Nk_max;
+  a.d = d;
+  a.num_splits = num_splits;
+  a.chunk = fa_decode_chunk(Nk_max, num_splits);
+  a.scale = scale;
+  a.bf16 = dt == FA_BF16 ? 1 : 0;
+  a.status = fa::device_status_word();
+  if (!a.status) return FA_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = fa::launch_cache_decode(a, 0, s);
+  if (e == cudaSuccess) e = fa::launch_cache_combine(a, s);
+  return from_cuda(e);
+}
+
+// Keys per prefix split: ceil(Np / splits) rounded up to a 128-key tile.
+static int prefix_chunk(int Np, int splits) { return ((Np + splits - 1) / splits + 127) / 128 * 128; }
+
+int fa_decode_prefix_splits(int B, int Hq, int Hkv, int Np, int num_sms) {
+  if (B < 1 || Hq < 1 || Hkv < 1 || Np < 1 || Hq % Hkv != 0 || Hq / Hkv > 128) return 1;
+  const int seqs = 128 / (Hq / Hkv);  // sequences per 128-row query tile, two tiles per CTA
+  const long long units = (long long)Hkv * ((B + 2 * seqs - 1) / (2 * seqs));
+  const int tiles = (Np + 127) / 128, sms = sm_count(num_sms);
+  // rounds of the SMs times a work's length in tiles, 3 of them for its start and end
+  int best = 1;
+  long long cost = -1;
+  for (int s = 1; s <= std::min(tiles, 256); ++s) {
+    const int per = (tiles + s - 1) / s;
+    if ((tiles + per - 1) / per != s) continue;  // the same lengths with fewer splits
+    const long long c = ((units * s + sms - 1) / sms) * (per + 3);
+    if (cost < 0 || c < cost) {
+      cost = c;
+      best = s;
+    }
+  }
+  return best;
+}
+
+fa_status fa_decode_shared_prefix(const void* q, const void* k_prefix, const void* v_prefix, const void* k_cache,
+                                  const void* v_cache, const float* k_scale, const float* v_scale,
+                                  const int* seqlens_k, void* o, float* lse, void* workspace, int B, int Hq, int Hkv,
+                                  int Np, int Nk_max, int d, float scale, int prefix_splits, int num_splits,
+                                  fa_dtype dt, fa_stream_t stream) {
+  if (!q || !k_prefix || !v_prefix || !k_cache || !v_cache || !seqlens_k || !o || !lse || !workspace)
+    return FA_ERR_INVALID;
+  if ((k_scale == nullptr) != (v_scale == nullptr)) return FA_ERR_INVALID;
+  const fa_status st = check_decode(B, Hq, Hkv, Nk_max, d, scale, num_splits, dt);
+  if (st != FA_OK) return st;
+  if (Np < 1 || prefix_splits < 1) return FA_ERR_INVALID;
+  if (Np > (1 << 30) || prefix_splits > 65535) return FA_ERR_UNSUPPORTED;
+  if (prefix_splits > (Np + 127) / 128) return FA_ERR_INVALID;
+  const int pchunk = prefix_chunk(Np, prefix_splits);
+  if ((long long)(prefix_splits - 1) * pchunk >= Np) return FA_ERR_INVALID;  // the last split would be empty
+  if (!aligned(q, 16) || !aligned(k_prefix, 16) || !aligned(v_prefix, 16) || !aligned(k_cache, 16) ||
+      !aligned(v_cache, 16) || !aligned(o, 16) || !aligned(workspace, 16) || !aligned(k_scale, 4) ||
+      !aligned(v_scale, 4) || !aligned(seqlens_k, 4) || !aligned(lse, 4))
+    return FA_ERR_ALIGN;
+  if (!fa::tma_available()) return FA_ERR_CUDA;  // the driver lacks the tensor-map encoder
+  fa::CacheDecodeArgs a{};
+  a.q = q;
+  a.kp = k_prefix;
+  a.vp = v_prefix;
+  a.k = k_cache;
+  a.v = v_cache;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.seqlens = seqlens_k;
+  a.o_part = static_cast<float*>(workspace);
+  a.lse_part = a.o_part + (size_t)B * Hq * (prefix_splits + num_splits) * d;
+  a.o = o;
+  a.lse = lse;
+  a.B = B;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.Np = Np;
+  a.Nk_max = Nk_max;
+  a.d = d;
+  a.prefix_splits = prefix_splits;
+  a.prefix_chunk = pchunk;
+  a.num_splits = num_splits;
+  a.chunk = fa_decode_chunk(Nk_max, num_splits);
+  a.scale = scale;
+  a.bf16 = dt == FA_BF16 ? 1 : 0;
+  a.status = fa::device_status_word();
+  if (!a.status) return FA_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = fa::launch_prefix_sm100(a, s);
+  if (e == cudaSuccess) e = fa::launch_cache_decode(a, 1, s);
+  if (e == cudaSuccess) e = fa::launch_cache_combine(a, s);
+  return from_cuda(e);
+}
+
+}  // extern "C"

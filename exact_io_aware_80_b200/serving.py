@@ -1,0 +1,291 @@
+"""Rotary positions, an E4M3 key/value cache, and decode over it or behind a shared prefix.
+
+PyTorch-facing wrappers of the entry points of the same kinds in ``include/fa.h``.
+As in the package's other wrappers only tensor metadata is checked, outputs and
+workspaces are allocated with PyTorch, and raw pointers plus the current CUDA
+stream go to libfa.so; there is no CPU or PyTorch fallback.
+
+Layouts: q, o [B, N, Hq, d]; k, v [B, N, Hkv, d]; an E4M3 cache is k8, v8
+[B, Nk_max, Hkv, d] uint8 with k_scale, v_scale [B, Hkv, Nk_max] float32;
+seqlens_k, start, counts int32 [B].
+"""
+from __future__ import annotations
+
+import math
+
+from . import _lib
+
+__all__ = ["rotary_table", "rotary_magnitude", "rotary_fwd", "rotary_bwd", "fp8_cache_append", "fp8_cache_read",
+           "decode_fp8", "decode_shared_prefix"]
+
+
+def _torch():
+    import torch
+    return torch
+
+
+def _dt(t):
+    torch = _torch()
+    if t.dtype == torch.bfloat16:
+        return _lib.FA_BF16
+    if t.dtype == torch.float16:
+        return _lib.FA_FP16
+    raise TypeError(f"attention tensors must be fp16 or bf16, got {t.dtype}")
+
+
+def _check(name, t, dtype, shape, dev, contiguous=True):
+    if t.device != dev or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor on the device of the first argument (no CPU path)")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _call(dev, fn, *args):
+    """fn(*args, stream) with ``dev`` current, on its current stream."""
+    cuda = _torch().cuda
+    if dev.index == cuda.current_device():
+        fn(*args, cuda.current_stream(dev).cuda_stream)
+    else:
+        with cuda.device(dev):
+            fn(*args, cuda.current_stream(dev).cuda_stream)
+
+
+def _strides(name, t):
+    """(batch, token) strides of [B, N, H, d] whose heads are contiguous."""
+    B, N, H, d = t.shape
+    st = t.stride()
+    if (st[3] != 1 and d > 1) or (st[2] != d and H > 1):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return (st[0] if B > 1 else 0), (st[1] if N > 1 else 0)
+
+
+# ---------------------------------------------------------------------------
+# rotary positions
+# ---------------------------------------------------------------------------
+def rotary_table(rot_dim: int, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
+                 original_len: int | None = None, low_turns: float = 1.0, high_turns: float = 32.0, device="cuda"):
+    """The frequencies f_i = base^(-2i / rot_dim) as the int64 table that the rotary calls take.
+
+    Entry i is f_i / (2 pi), turns per position, as a 64-bit fraction of one turn.  For contexts
+    longer than the trained one:
+
+    * ``scaling="linear"``: positions divided by ``factor``;
+    * ``scaling="ntk"``: base grown to base * factor^(rot_dim / (rot_dim - 2)), which divides the
+      lowest frequency by ``factor`` and leaves the highest;
+    * ``scaling="by_parts"``: with r = original_len f_i / (2 pi) turns over the trained context, f_i
+      is divided by ``factor`` for r <= low_turns, kept for r >= high_turns, and blended linearly in
+      r between them (see also :func:`rotary_magnitude`).
+    """
+    torch = _torch()
+    if rot_dim < 2 or rot_dim % 2:
+        raise ValueError(f"rot_dim must be even and at least 2, got {rot_dim}")
+    if not (base > 0 and math.isfinite(base)) or not (factor > 0 and math.isfinite(factor)):
+        raise ValueError("base and factor must be positive and finite")
+    if scaling not in (None, "linear", "ntk", "by_parts"):
+        raise ValueError(f"scaling must be None, 'linear', 'ntk' or 'by_parts', got {scaling!r}")
+    if scaling == "ntk":
+        if rot_dim < 4:
+            raise ValueError("scaling='ntk' needs rot_dim >= 4")
+        base = base * factor ** (rot_dim / (rot_dim - 2))
+    if scaling == "by_parts" and (original_len is None or original_len < 1 or not 0 <= low_turns < high_turns):
+        raise ValueError("scaling='by_parts' needs original_len >= 1 and 0 <= low_turns < high_turns")
+    turns = []
+    for i in range(rot_dim // 2):
+        f = base ** (-2.0 * i / rot_dim)
+        if scaling == "linear":
+            f /= factor
+        elif scaling == "by_parts":
+            r = original_len * f / (2 * math.pi)
+            keep = min(1.0, max(0.0, (r - low_turns) / (high_turns - low_turns)))
+            f = keep * f + (1.0 - keep) * f / factor
+        u = int(round(f / (2 * math.pi) * 2.0 ** 64)) % (1 << 64)
+        turns.append(u - (1 << 64) if u >= 1 << 63 else u)
+    return torch.tensor(turns, dtype=torch.int64, device=device)
+
+
+def rotary_magnitude(factor: float) -> float:
+    """0.1 ln(factor) + 1 (1 for factor <= 1): the ``magnitude`` that goes with ``by_parts`` scaling."""
+    return 0.1 * math.log(factor) + 1.0 if factor > 1 else 1.0
+
+
+def _rotary(q, k, positions, table, interleaved, magnitude, inverse, q_out, k_out):
+    torch = _torch()
+    dev = q.device
+    B, N, Hq, d = q.shape
+    dt = _dt(q)
+    _check("q", q, q.dtype, q.shape, dev, contiguous=False)
+    _check("table", table, torch.int64, table.shape[:1], dev)
+    _check("positions", positions, torch.int32, (N,) if positions.dim() == 1 else (B, N), dev)
+    q_st, k_st, Hkv, kp, kop = _strides("q", q), (0, 0), 0, 0, 0
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    else:
+        _check("q_out", q_out, q.dtype, q.shape, dev)
+    if k is not None:
+        Hkv = k.shape[2]
+        _check("k", k, q.dtype, (B, N, Hkv, d), dev, contiguous=False)
+        k_st = _strides("k", k)
+        if k_out is None:
+            k_out = torch.empty(k.shape, dtype=q.dtype, device=dev)
+        else:
+            _check("k_out", k_out, q.dtype, k.shape, dev)
+        kp, kop = k.data_ptr(), k_out.data_ptr()
+    _call(dev, _lib.fa_rotary, q.data_ptr(), kp, q_out.data_ptr(), kop, positions.data_ptr(), table.data_ptr(), B, N,
+          Hq, Hkv, d, 2 * table.numel(), interleaved, inverse, magnitude, *q_st, *k_st,
+          N if positions.dim() == 2 else 0, dt)
+    return q_out, k_out
+
+
+def rotary_fwd(q, k, positions, table, interleaved: bool = False, magnitude: float = 1.0, q_out=None, k_out=None):
+    """q and k turned by their tokens' positions, via ``fa_rotary``; returns (q, k).
+
+    ``positions``: int32 [B, N], or [N] shared by the batch; ``table``: from :func:`rotary_table`, its
+    rot_dim at most d (later values of each head are copied).  q and k may be slices of one packed
+    projection (heads contiguous); k may be None.  Outputs are contiguous; ``q_out=q`` (``k_out=k``)
+    works in place on a contiguous tensor.
+    """
+    return _rotary(q, k, positions, table, interleaved, magnitude, False, q_out, k_out)
+
+
+def rotary_bwd(dq, dk, positions, table, interleaved: bool = False, magnitude: float = 1.0, q_out=None, k_out=None):
+    """Gradients with respect to :func:`rotary_fwd`'s q and k from those of its outputs: the transpose
+    of the rotation, with the same positions, table, layout and magnitude."""
+    return _rotary(dq, dk, positions, table, interleaved, magnitude, True, q_out, k_out)
+
+
+# ---------------------------------------------------------------------------
+# the E4M3 cache
+# ---------------------------------------------------------------------------
+def _check_cache(k8, v8, k_scale, v_scale, B, Hkv, d, dev):
+    torch = _torch()
+    Nk_max = k8.shape[1]
+    _check("k8", k8, torch.uint8, (B, Nk_max, Hkv, d), dev)
+    _check("v8", v8, torch.uint8, (B, Nk_max, Hkv, d), dev)
+    _check("k_scale", k_scale, torch.float32, (B, Hkv, Nk_max), dev)
+    _check("v_scale", v_scale, torch.float32, (B, Hkv, Nk_max), dev)
+    return Nk_max
+
+
+def fp8_cache_append(k, v, k8, v8, k_scale, v_scale, start, counts=None):
+    """Quantise k, v [B, n, Hkv, d] into rows start[b] .. of an E4M3 cache, in place, via ``fa_fp8_cache_append``.
+
+    ``counts``: int32 [B], rows that each sequence appends (None: all n).  Rows that fall outside the
+    cache are dropped.  k and v may be slices of one packed projection (heads contiguous).
+    """
+    torch = _torch()
+    dev = k.device
+    B, n, Hkv, d = k.shape
+    dt = _dt(k)
+    _check("k", k, k.dtype, k.shape, dev, contiguous=False)
+    _check("v", v, k.dtype, k.shape, dev, contiguous=False)
+    Nk_max = _check_cache(k8, v8, k_scale, v_scale, B, Hkv, d, dev)
+    _check("start", start, torch.int32, (B,), dev)
+    if counts is not None:
+        _check("counts", counts, torch.int32, (B,), dev)
+    _call(dev, _lib.fa_fp8_cache_append, k.data_ptr(), v.data_ptr(), k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(),
+          v_scale.data_ptr(), start.data_ptr(), 0 if counts is None else counts.data_ptr(), B, n, Hkv, Nk_max, d,
+          *_strides("k", k), *_strides("v", v), dt)
+
+
+def fp8_cache_read(k8, v8, k_scale, v_scale, seqlens_k, Nk: int | None = None, dtype=None):
+    """The first Nk rows (None: all) of an E4M3 cache as (k, v) [B, Nk, Hkv, d] in ``dtype`` (bf16 by
+    default), rows past seqlens_k[b] zero, via ``fa_fp8_cache_read``."""
+    torch = _torch()
+    dev = k8.device
+    B, Nk_max, Hkv, d = k8.shape
+    _check_cache(k8, v8, k_scale, v_scale, B, Hkv, d, dev)
+    _check("seqlens_k", seqlens_k, torch.int32, (B,), dev)
+    Nk = Nk_max if Nk is None else Nk
+    k = torch.empty(B, Nk, Hkv, d, dtype=torch.bfloat16 if dtype is None else dtype, device=dev)
+    v = torch.empty_like(k)
+    _call(dev, _lib.fa_fp8_cache_read, k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+          seqlens_k.data_ptr(), k.data_ptr(), v.data_ptr(), B, Nk, Hkv, Nk_max, d, _dt(k))
+    return k, v
+
+
+# ---------------------------------------------------------------------------
+# decode
+# ---------------------------------------------------------------------------
+def _decode_buffers(q, seqlens_k, splits, workspace, out, lse):
+    torch = _torch()
+    dev = q.device
+    B, Nq, Hq, d = q.shape
+    _check("q", q, q.dtype, (B, 1, Hq, d), dev)
+    _check("seqlens_k", seqlens_k, torch.int32, (B,), dev)
+    need = _lib.fa_decode_workspace_bytes(B, Hq, splits, d)
+    if workspace is None:
+        workspace = torch.empty(need, device=dev, dtype=torch.uint8)
+    elif workspace.device != dev or not workspace.is_contiguous() or \
+            workspace.numel() * workspace.element_size() < need:
+        raise ValueError(f"workspace must be contiguous, on the device of q and hold {need} bytes")
+    if out is None:
+        out = torch.empty(B, 1, Hq, d, device=dev, dtype=q.dtype)
+    else:
+        _check("out", out, q.dtype, (B, 1, Hq, d), dev)
+    if lse is None:
+        lse = torch.empty(B, Hq, 1, device=dev, dtype=torch.float32)
+    else:
+        _check("lse", lse, torch.float32, (B, Hq, 1), dev)
+    return workspace, out, lse
+
+
+def decode_fp8(q, k8, v8, k_scale, v_scale, seqlens_k, num_splits: int | None = None, scale: float | None = None,
+               workspace=None, out=None, lse=None):
+    """One-token attention over an E4M3 cache; returns O [B, 1, Hq, d] and LSE [B, Hq, 1] (``fa_decode_fp8``)."""
+    dev = q.device
+    B, _, Hq, d = q.shape
+    Hkv = k8.shape[2]
+    dt = _dt(q)
+    Nk_max = _check_cache(k8, v8, k_scale, v_scale, B, Hkv, d, dev)
+    scale = 1.0 / math.sqrt(d) if scale is None else scale
+    if num_splits is None:
+        num_splits = _lib.fa_decode_fp8_num_splits(B, Hkv, Nk_max)
+    workspace, out, lse = _decode_buffers(q, seqlens_k, num_splits, workspace, out, lse)
+    _call(dev, _lib.fa_decode_fp8, q.data_ptr(), k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+          seqlens_k.data_ptr(), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), B, Hq, Hkv, Nk_max, d, scale,
+          num_splits, dt)
+    return out, lse
+
+
+def decode_shared_prefix(q, k_prefix, v_prefix, k_cache, v_cache, seqlens_k, k_scale=None, v_scale=None,
+                         prefix_splits: int | None = None, num_splits: int | None = None, scale: float | None = None,
+                         workspace=None, out=None, lse=None):
+    """One-token attention of a batch behind one prefix; returns O [B, 1, Hq, d] and LSE [B, Hq, 1].
+
+    Every sequence sees all of ``k_prefix``, ``v_prefix`` [1, Np, Hkv, d] and then the first
+    seqlens_k[b] rows (0 allowed) of its own cache, [B, Nk_max, Hkv, d] in q's type, or uint8 E4M3
+    codes with ``k_scale`` and ``v_scale`` (``fa_decode_shared_prefix``).
+    """
+    torch = _torch()
+    dev = q.device
+    B, _, Hq, d = q.shape
+    Np, Hkv = k_prefix.shape[1:3]
+    dt = _dt(q)
+    _check("k_prefix", k_prefix, q.dtype, (1, Np, Hkv, d), dev)
+    _check("v_prefix", v_prefix, q.dtype, (1, Np, Hkv, d), dev)
+    if k_cache.dtype == torch.uint8:
+        if k_scale is None or v_scale is None:
+            raise ValueError("an E4M3 cache comes with k_scale and v_scale")
+        Nk_max = _check_cache(k_cache, v_cache, k_scale, v_scale, B, Hkv, d, dev)
+        ksp, vsp = k_scale.data_ptr(), v_scale.data_ptr()
+    else:
+        if k_scale is not None or v_scale is not None:
+            raise ValueError("k_scale and v_scale go with uint8 E4M3 caches")
+        Nk_max = k_cache.shape[1]
+        _check("k_cache", k_cache, q.dtype, (B, Nk_max, Hkv, d), dev)
+        _check("v_cache", v_cache, q.dtype, (B, Nk_max, Hkv, d), dev)
+        ksp = vsp = 0
+    scale = 1.0 / math.sqrt(d) if scale is None else scale
+    if prefix_splits is None:
+        prefix_splits = _lib.fa_decode_prefix_splits(B, Hq, Hkv, Np)
+    if num_splits is None:
+        num_splits = _lib.fa_decode_fp8_num_splits(B, Hkv, Nk_max)
+    workspace, out, lse = _decode_buffers(q, seqlens_k, prefix_splits + num_splits, workspace, out, lse)
+    _call(dev, _lib.fa_decode_shared_prefix, q.data_ptr(), k_prefix.data_ptr(), v_prefix.data_ptr(),
+          k_cache.data_ptr(), v_cache.data_ptr(), ksp, vsp, seqlens_k.data_ptr(), out.data_ptr(), lse.data_ptr(),
+          workspace.data_ptr(), B, Hq, Hkv, Np, Nk_max, d, scale, prefix_splits, num_splits, dt)
+    return out, lse

@@ -351,6 +351,103 @@ fa_status fa_bwd_accumulate(const void* q, const void* k, const void* v, const v
 fa_status fa_accumulate(float* acc, const void* part, long long n, int init, fa_dtype dt, fa_stream_t stream);
 fa_status fa_cast_f32(const float* acc, void* out, long long n, fa_dtype dt, fa_stream_t stream);
 
+/* ------------------------------------------------------------------------------
+ * Around the attention calls: rotary positions, a key/value cache in E4M3, and
+ * decode over that cache or behind a prefix that a whole batch shares.  The
+ * pages describe none of these; the definitions are stated here.
+ * ---------------------------------------------------------------------------- */
+
+/*
+ * Rotary positions of queries and keys, in one launch.  Of each head's d values
+ * the first rot_dim form pairs, (x[i], x[i + rot_dim/2]) or, `interleaved`,
+ * (x[2i], x[2i+1]); pair i of the token at position p is turned by the angle
+ * t = p f_i and scaled by `magnitude` m,
+ *   y0 = m (x0 cos t - x1 sin t),  y1 = m (x1 cos t + x0 sin t),
+ * and values past rot_dim are copied.  `inverse` turns by -t: the transpose of
+ * the map, so it takes gradients with respect to q_out and k_out to gradients
+ * with respect to q and k.
+ *   q [B,N,Hq,d], k [B,N,Hkv,d]: heads contiguous, tokens and batches at the
+ *     given strides (elements, multiples of 8), e.g. slices of one packed
+ *     projection.  k and k_out may be NULL with Hkv = 0.
+ *   q_out, k_out: contiguous; each either its own input (in place, which must
+ *     then be contiguous too) or apart from every other tensor here.
+ *   positions: DEVICE int32, position of token n of sequence b at
+ *     b * position_batch_stride + n; position_batch_stride 0 shares one row of
+ *     N positions.  Any int32 value.
+ *   turns: DEVICE uint64 [rot_dim/2], f_i / (2 pi) turns per position as a
+ *     fraction of one turn in units of 2^-64, so that p turns_i modulo 2^64 is
+ *     the phase, exact to |p| 2^-65 turns at any position.
+ * rot_dim a multiple of 16, at most d; d 64 or 128; B * N < 2^31.
+ */
+fa_status fa_rotary(const void* q, const void* k, void* q_out, void* k_out, const int* positions,
+                    const unsigned long long* turns, int B, int N, int Hq, int Hkv, int d, int rot_dim,
+                    int interleaved, int inverse, float magnitude, long long q_batch_stride,
+                    long long q_token_stride, long long k_batch_stride, long long k_token_stride,
+                    long long position_batch_stride, fa_dtype dt, fa_stream_t stream);
+
+/*
+ * Key and value rows quantised to E4M3 as they enter a cache.  One fp32 scale
+ * per (token, head), s = amax / 448 (1 for a row of zeros), code = E4M3(x / s)
+ * rounded to nearest even with IEEE fp32 divisions.  A row with a NaN or an
+ * infinity reads back as NaN throughout.
+ *   k, v [B,n,Hkv,d] 16-bit (dt): heads contiguous, tokens and batches at the
+ *     given strides (elements, multiples of 8).
+ *   k8, v8 [B,Nk_max,Hkv,d] bytes; k_scale, v_scale [B,Hkv,Nk_max] fp32.
+ *   start: DEVICE int32 [B], the cache row of each sequence's first new token;
+ *   counts: DEVICE int32 [B] or NULL, how many of the n rows a sequence appends
+ *     (NULL: all n; values outside [0, n] are clamped into that range).
+ * Rows whose place lies outside [0, Nk_max) are dropped, and every other row of
+ * the cache is left as it was.
+ */
+fa_status fa_fp8_cache_append(const void* k, const void* v, void* k8, void* v8, float* k_scale, float* v_scale,
+                              const int* start, const int* counts, int B, int n, int Hkv, int Nk_max, int d,
+                              long long k_batch_stride, long long k_token_stride, long long v_batch_stride,
+                              long long v_token_stride, fa_dtype dt, fa_stream_t stream);
+
+/*
+ * The first Nk (<= Nk_max) rows of such a cache as 16-bit values (code times
+ * scale, rounded once): k, v [B,Nk,Hkv,d], as fa_fwd takes them.  Rows at or
+ * past seqlens_k[b] (DEVICE int32 [B]) are written as zeros.
+ */
+fa_status fa_fp8_cache_read(const void* k8, const void* v8, const float* k_scale, const float* v_scale,
+                            const int* seqlens_k, void* k, void* v, int B, int Nk, int Hkv, int Nk_max, int d,
+                            fa_dtype dt, fa_stream_t stream);
+
+/* Suggested number of key splits for fa_decode_fp8 (num_sms <= 0: query the current device). */
+int fa_decode_fp8_num_splits(int B, int Hkv, int Nk_max, int num_sms);
+
+/*
+ * One-token attention over an E4M3 cache (fa_fp8_cache_append): q [B,1,Hq,d] and
+ * o [B,1,Hq,d] 16-bit (dt), lse [B,Hq,1] fp32; each sequence sees its first
+ * seqlens_k[b] rows (DEVICE int32 [B], clamped into [0, Nk_max]); a sequence of
+ * length 0 gets O = 0 and LSE = -inf.  The keys are cut into num_splits ranges
+ * of fa_decode_chunk(Nk_max, num_splits) and merged by log-sum-exp; workspace
+ * of fa_decode_workspace_bytes(B, Hq, num_splits, d) bytes.  scale >= 0, finite;
+ * at most 16 query heads per KV head.  Scales in the cache are positive.
+ */
+fa_status fa_decode_fp8(const void* q, const void* k8, const void* v8, const float* k_scale, const float* v_scale,
+                        const int* seqlens_k, void* o, float* lse, void* workspace, int B, int Hq, int Hkv,
+                        int Nk_max, int d, float scale, int num_splits, fa_dtype dt, fa_stream_t stream);
+
+/* Suggested number of prefix splits for fa_decode_shared_prefix (num_sms <= 0: query the current device). */
+int fa_decode_prefix_splits(int B, int Hq, int Hkv, int Np, int num_sms);
+
+/*
+ * One-token attention of a batch whose sequences share their first Np keys:
+ * sequence b sees k_prefix, v_prefix [Np,Hkv,d] (16-bit, dt), computed once for
+ * all sequences, followed by the first seqlens_k[b] rows of its own cache.
+ * k_cache, v_cache [B,Nk_max,Hkv,d]: 16-bit (dt) with k_scale and v_scale NULL,
+ * or E4M3 codes with scales [B,Hkv,Nk_max].  q, o, lse, seqlens_k and limits as
+ * fa_decode_fp8.  The prefix is cut into prefix_splits ranges of whole 128-key
+ * tiles, none of them empty, the caches into num_splits; workspace of
+ * fa_decode_workspace_bytes(B, Hq, prefix_splits + num_splits, d) bytes.
+ */
+fa_status fa_decode_shared_prefix(const void* q, const void* k_prefix, const void* v_prefix, const void* k_cache,
+                                  const void* v_cache, const float* k_scale, const float* v_scale,
+                                  const int* seqlens_k, void* o, float* lse, void* workspace, int B, int Hq,
+                                  int Hkv, int Np, int Nk_max, int d, float scale, int prefix_splits,
+                                  int num_splits, fa_dtype dt, fa_stream_t stream);
+
 /*
  * Synchronises `stream`, then reads and clears the device status word that the
  * kernels set when a bounded wait runs out (FA_ERR_TIMEOUT) or, in the checking
