@@ -10,25 +10,35 @@
 // s^v_j the weight, so a key costs its d + 4 bytes twice.
 //
 // Partial pass: one CTA per (split, KV head, sequence).  The group's Hq / Hkv
-// query rows (padded to the 16-row MMA shape) share every byte the CTA reads.
-// Tiles of 64 keys stream through a cp.async ring; each of the four warps takes
-// 16 keys of a tile with its own running (m, l, O), merged through shared
-// memory at the end.  Bound by HBM reads of the cache.
+// query rows share every byte the CTA reads.  Each of the four warps streams
+// its own blocks of kStep keys through its own cp.async ring (no block barrier
+// until the end) with its own running (m, l, O); the warps merge through shared
+// memory.  Bound by HBM reads of the cache as long as the arithmetic per key is
+// small, which shapes the rest:
+//  * The products are taken transposed, S^T = K Q^T and O^T = V^T P^T, so that
+//    keys and columns of d fill the MMA's 16 rows and the group its 8 columns
+//    (two column blocks for groups of 9 to 16): half the MMAs, exponentials and
+//    accumulators of padding the group to 16 rows.
+//  * m is a reference that stays until a score exceeds it by more than 2^6:
+//    then every lane's maximum is reduced and O, l rescaled; otherwise a block
+//    costs one vote.
 //
 // E4M3 operands.  E4M3 values are exact in fp16, so codes are converted in
 // registers (cvt.rn.f16x2.e4m3x2) and multiplied as m16n8k16 fp16 products:
-//  * K: the four threads of a key's row read 16 consecutive codes each; the
-//    order in which the MMA's k index runs over d is free as long as q follows
-//    it, so q is loaded in the same order.
+//  * K: an 8 x 16-byte ldmatrix gives a thread four consecutive codes of a key;
+//    the order in which the MMA's k index runs over d is free as long as q
+//    follows it, so q is loaded in that order.
 //  * V: the transposing ldmatrix moves 16-bit units, here two neighbouring
 //    columns of one key; a byte permutation per register gives the key pairs of
-//    either column, so an n8 block of the MMA holds every second column.
+//    either column, so rows r and r + 8 of an MMA are columns 2 r and 2 r + 1.
 //  * q in bf16 is scaled by a power of two per row that brings its largest
 //    value to [2^14, 2^15): conversion to fp16 is then exact for every element
 //    within 2^-30 of the row's largest and off by at most 2^-39 of it below.
-//  * the weights p_j s^v_j are fp16 in units of 2^(e - 14), where 2^e exceeds
-//    every s^v seen so far: at most 2^14, relative error 2^-11 down to 2^-28 of
-//    the unit's largest, absolute 2^-39 of it below.  l sums the unrounded p_j.
+//  * the weights p_j s^v_j are fp16 in units of 2^(e - 8), where 2^e exceeds
+//    every s^v seen so far: at most 2^14 (p up to 2^6), relative error 2^-11
+//    down to 2^-22 of 2^e, absolute 2^-33 of it below.
+// l sums the unrounded p_j.  fp16 weights of a 16-bit cache are kept 2^8 larger
+// (m lowered by 8) for the same reason: at most 2^14, normal down to 2^-22.
 #include <math.h>
 
 #include <type_traits>
@@ -40,111 +50,68 @@ namespace fa {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kTileN = 64;  // keys per tile
-constexpr int kStages = 3;
-constexpr int kRows = 16;  // MMA rows: the group's query heads, zero-padded
+constexpr float kStale = 6.f;  // log2 units that a score may exceed the reference m by
+constexpr int kMinUnit = -112;  // smallest e of the weights' unit (all powers of two below stay normal)
 
-// Byte offset of 16-byte chunk `c` of key row `r` in a tile of E4M3 rows of D bytes.  Chunks are
-// permuted so that both the K reads (two rows x four chunks per quarter-warp) and the V reads
-// (ldmatrix: one chunk of eight rows) touch every bank once.
-template <int D>
-__device__ __forceinline__ uint32_t chunk8(int r, int c) {
-  if constexpr (D == 128)
-    return r * 128 + ((c ^ (((r & 1) << 2) | ((r >> 1) & 3))) << 4);
-  else
-    return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
-}
+// Shape of a warp's ring: kStep keys a block, kStages blocks.
+template <int D, bool F8>
+struct Ring {
+  static constexpr int kRow = D * (F8 ? 1 : 2);          // bytes of a K or V row
+  static constexpr int kStep = kRow <= 128 ? 32 : 16;    // keys per block
+  static constexpr int kStages = 3;
+  static constexpr int kTile = kStep * kRow;
+  static constexpr int kStage = 2 * kTile + (F8 ? 2 * kStep * 4 : 0);  // K, V, their scales
+  static constexpr int kWarp = kStages * kStage;
+  static constexpr int kBlocks = kStep / 16;
+};
+template <int D, bool F8, int NB>
+struct Smem {
+  static constexpr int kRed = (4 * 8 * NB * (D + 2)) * 4;
+  static constexpr int kBytes = 4 * Ring<D, F8>::kWarp > kRed ? 4 * Ring<D, F8>::kWarp : kRed;
+};
 
-template <int D>
-__device__ __forceinline__ void load_codes_async(uint32_t smem, const uint8_t* g, int row0, int nrows, long ld,
-                                                 int tid) {
-  constexpr int kC = D / 16;
-#pragma unroll
-  for (int e = tid; e < kTileN * kC; e += kThreads) {
-    const int r = e / kC, c = e % kC;
-    const bool ok = row0 + r < nrows;
-    cp_async16(smem + chunk8<D>(r, c), g + (ok ? (long)(row0 + r) * ld + 16 * c : 0), ok);
-  }
+// Byte offset of 16-byte chunk `c` of row `r` in a tile of ROW-byte rows, chunks permuted so that
+// one chunk of eight consecutive rows (ldmatrix) touches every bank once.
+template <int ROW>
+__device__ __forceinline__ uint32_t chunk_at(int r, int c) {
+  return r * ROW + ((c ^ (ROW >= 128 ? (r & 7) : ((r >> 1) & 3))) << 4);
 }
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool valid) {
   const int n = valid ? 4 : 0;
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(dst), "l"(src), "r"(n));
 }
-
-// Two E4M3 codes (low byte first) as an fp16 pair; exact.
-__device__ __forceinline__ uint32_t e4m3_to_h2(uint32_t two) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)two));
-  return r;
+// Four E4M3 codes (low byte first) as two fp16 pairs; exact.
+__device__ __forceinline__ void e4m3x4_to_h2(uint32_t four, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(four));
 }
-__device__ __forceinline__ uint32_t e4m3_to_h2_hi(uint32_t four) { return e4m3_to_h2(four >> 16); }
-
-// q's rows lane / 4 and lane / 4 + 8 as fp16 A fragments in the order of the K codes: MMA step
-// 4 g + i of 16-key-column group g takes, for the thread with c = lane & 3, columns
-// 64 g + 16 c + 4 i .. + 3.  Returns 2^-k of the power of two each row was multiplied by.
-template <typename T, int D>
-__device__ __forceinline__ void load_q8(uint32_t (&qf)[D / 16][4], float (&unscale)[2], const uint16_t* gq, int G,
-                                        int lane) {
-  const int c = lane & 3;
-  float x[2][D / 4];
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const int r = (lane >> 2) + 8 * e;
-    float amax = 0.f;
-#pragma unroll
-    for (int g = 0; g < D / 64; ++g)
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        uint4 w = make_uint4(0u, 0u, 0u, 0u);
-        if (r < G) w = *reinterpret_cast<const uint4*>(gq + (long)r * D + 64 * g + 16 * c + 8 * k);
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 f = Elem<T>::unpack(u[i]);
-          x[e][16 * g + 8 * k + 2 * i] = f.x;
-          x[e][16 * g + 8 * k + 2 * i + 1] = f.y;
-          amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
-        }
-      }
-    amax = quad_max(amax);
-    float mul = 1.f;
-    unscale[e] = 1.f;
-    if constexpr (Elem<T>::kBf16) {
-      // exponent of amax, kept where both powers of two are normal numbers
-      int ex = (int)(__float_as_uint(amax) >> 23) - 127;
-      ex = min(max(ex, -100), 126);
-      mul = __uint_as_float((uint32_t)(14 - ex + 127) << 23);
-      unscale[e] = __uint_as_float((uint32_t)(ex - 14 + 127) << 23);
-    }
-#pragma unroll
-    for (int i = 0; i < D / 4; ++i) x[e][i] *= mul;
-  }
-#pragma unroll
-  for (int s = 0; s < D / 16; ++s) {
-    const int i = 4 * s;
-    qf[s][0] = Elem<__half>::pack(x[0][i], x[0][i + 1]);
-    qf[s][1] = Elem<__half>::pack(x[1][i], x[1][i + 1]);
-    qf[s][2] = Elem<__half>::pack(x[0][i + 2], x[0][i + 3]);
-    qf[s][3] = Elem<__half>::pack(x[1][i + 2], x[1][i + 3]);
-  }
+// Transpose of an 8 x 8 matrix of 16-bit values held as ldmatrix leaves it.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+// Maximum and sum over the lanes that hold the same query rows (lane & 3 equal).
+__device__ __forceinline__ float rows_max(float x) {
+  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+  return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+}
+__device__ __forceinline__ float rows_sum(float x) {
+  x += __shfl_xor_sync(0xffffffffu, x, 4);
+  x += __shfl_xor_sync(0xffffffffu, x, 8);
+  return x + __shfl_xor_sync(0xffffffffu, x, 16);
 }
 
-template <typename T, int D, bool F8>
-struct Smem {
-  static constexpr int kTile = kTileN * D * (F8 ? 1 : 2);
-  static constexpr int kScales = F8 ? 2 * kTileN * 4 : 0;
-  static constexpr int kStage = 2 * kTile + kScales;  // K, V, then their scales
-  static constexpr int kOffStage = F8 ? 0 : kRows * D * 2;  // 16-bit: q first
-  static constexpr int kPipe = kOffStage + kStages * kStage;
-  static constexpr int kRed = kOffStage + (4 * kRows * D + 8 * kRows) * 4;
-  static constexpr int kBytes = kPipe > kRed ? kPipe : kRed;
-};
-
-template <typename T, int D, bool F8>
+template <typename T, int D, bool F8, int NB>
 __global__ void __launch_bounds__(kThreads) cache_decode_kernel(CacheDecodeArgs p) {
   extern __shared__ __align__(1024) uint8_t smem[];
-  using L = Smem<T, D, F8>;
-  const uint32_t sb = smem_u32(smem);
+  using R = Ring<D, F8>;
+  using M = typename std::conditional<F8, __half, T>::type;  // MMA operand type
+  constexpr int MB = R::kBlocks;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int s = blockIdx.x, hk = blockIdx.y, b = blockIdx.z;
   const int G = p.Hq / p.Hkv;
@@ -157,203 +124,295 @@ __global__ void __launch_bounds__(kThreads) cache_decode_kernel(CacheDecodeArgs 
   // grid's end before it reads a partial
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (hi > lo) {
-    const int ntiles = (hi - lo + kTileN - 1) / kTileN;
-    const long ldk = (long)p.Hkv * D;
-    const uint16_t* gq = static_cast<const uint16_t*>(p.q) + ((long)b * p.Hq + (long)hk * G) * D;
-    const long base = ((long)b * p.Nk_max * p.Hkv + hk) * D;
+    const uint32_t ring = smem_u32(smem) + warp * R::kWarp;
+    const uint8_t* const ring_g = smem + warp * R::kWarp;
+    const long row_bytes = (long)p.Hkv * R::kRow;
+    const long base = ((long)b * p.Nk_max * p.Hkv + hk) * R::kRow;
+    const uint8_t* const gk = static_cast<const uint8_t*>(p.k) + base;
+    const uint8_t* const gv = static_cast<const uint8_t*>(p.v) + base;
     const long sbase = ((long)b * p.Hkv + hk) * p.Nk_max;
+    // this warp's blocks: keys lo + (4 i + warp) kStep ..
+    const int first = lo + warp * R::kStep;
+    const int nblk = first < hi ? (hi - first + 4 * R::kStep - 1) / (4 * R::kStep) : 0;
 
-    auto load_tile = [&](int t) {
-      const uint32_t st = sb + L::kOffStage + (t % kStages) * L::kStage;
+    constexpr int kC = R::kRow / 16, kRows = 32 / kC;  // chunks per row, rows per pass of the warp
+    const int lr = lane / kC, lc = lane % kC;
+    auto load = [&](int i) {
+      const uint32_t st = ring + (i % R::kStages) * R::kStage;
+      const int key0 = first + i * 4 * R::kStep;
+      if (key0 + R::kStep <= hi) {
+        const uint8_t* pk = gk + (long)(key0 + lr) * row_bytes + 16 * lc;
+        const uint8_t* pv = gv + (long)(key0 + lr) * row_bytes + 16 * lc;
+#pragma unroll
+        for (int j = 0; j < R::kStep / kRows; ++j) {
+          cp_async16(st + chunk_at<R::kRow>(lr + j * kRows, lc), pk, true);
+          cp_async16(st + R::kTile + chunk_at<R::kRow>(lr + j * kRows, lc), pv, true);
+          pk += kRows * row_bytes;
+          pv += kRows * row_bytes;
+        }
+      } else {  // the last block: rows past hi as zeros
+#pragma unroll 1
+        for (int j = 0; j < R::kStep / kRows; ++j) {
+          const int r = lr + j * kRows;
+          const bool ok = key0 + r < hi;
+          const long off = ok ? (long)(key0 + r) * row_bytes + 16 * lc : 0;
+          cp_async16(st + chunk_at<R::kRow>(r, lc), gk + off, ok);
+          cp_async16(st + R::kTile + chunk_at<R::kRow>(r, lc), gv + off, ok);
+        }
+      }
       if constexpr (F8) {
-        load_codes_async<D>(st, static_cast<const uint8_t*>(p.k) + base, lo + t * kTileN, hi, ldk, tid);
-        load_codes_async<D>(st + L::kTile, static_cast<const uint8_t*>(p.v) + base, lo + t * kTileN, hi, ldk, tid);
-        const int r = tid & 63, key = lo + t * kTileN + r;
-        const bool ok = key < hi;
-        const float* src = tid < 64 ? p.k_scale : p.v_scale;
-        cp_async4(st + 2 * L::kTile + tid * 4, src + sbase + (ok ? key : 0), ok);
-      } else {
-        load_tile_async<kTileN, D, kThreads>(st, static_cast<const uint16_t*>(p.k) + base, lo + t * kTileN, hi, ldk,
-                                             tid);
-        load_tile_async<kTileN, D, kThreads>(st + L::kTile, static_cast<const uint16_t*>(p.v) + base, lo + t * kTileN,
-                                             hi, ldk, tid);
+        const int r = lane % R::kStep;
+        const bool ok = key0 + r < hi;
+        cp_async4(st + 2 * R::kTile + 4 * r, p.k_scale + sbase + (ok ? key0 + r : 0), ok);
+        cp_async4(st + 2 * R::kTile + 4 * (R::kStep + r), p.v_scale + sbase + (ok ? key0 + r : 0), ok);
       }
     };
-    if constexpr (!F8) load_tile_async<kRows, D, kThreads>(sb, gq, 0, G, D, tid);
 #pragma unroll
-    for (int t = 0; t < kStages - 1; ++t) {
-      if (t < ntiles) load_tile(t);
+    for (int i = 0; i < R::kStages - 1; ++i) {
+      if (i < nblk) load(i);
       cp_async_commit();
     }
 
-    using M = typename std::conditional<F8, __half, T>::type;  // MMA operand type
-    float acc[D / 8][4];
+    // q as B fragments: column n = lane / 4 of block nb is query row 8 nb + n.  16-bit: k index =
+    // d; E4M3: k pairs 2c and 2c + 8 of step j are d = 16 j + 4 c + {0, 1} and {2, 3}, c = lane & 3
+    const uint16_t* gq = static_cast<const uint16_t*>(p.q) + ((long)b * p.Hq + (long)hk * G) * D;
+    uint32_t qf[NB][D / 16][2];
+    float cq[NB][2];  // scale log2(e) of rows 8 nb + 2 c + {0, 1}, without q's power of two
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-    float m_run[2] = {-INFINITY, -INFINITY};
-    float l_run[2] = {0.f, 0.f};
-    uint32_t qf[D / 16][4];
-    float c[2] = {p.scale * kLog2e, p.scale * kLog2e};
-    if constexpr (F8) {
-      float un[2];
-      load_q8<T, D>(qf, un, gq, G, lane);
-      c[0] *= un[0];
-      c[1] *= un[1];
-    }
-    int ev = -112;  // E4M3: 2^ev exceeds every V scale of this warp's keys so far
-
-    for (int t = 0; t < ntiles; ++t) {
-      if (t + kStages - 1 < ntiles) load_tile(t + kStages - 1);
-      cp_async_commit();
-      cp_async_wait<kStages - 1>();
-      __syncthreads();
-      const uint32_t st = sb + L::kOffStage + (t % kStages) * L::kStage;
-      if constexpr (!F8) {
-        if (t == 0) {
+    for (int nb = 0; nb < NB; ++nb) {
+      const int row = 8 * nb + (lane >> 2), c = lane & 3;
+      float mul = 1.f, unmul = 1.f;
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) frag_a<kRows>(qf[kk], sb, 0, kk * 16, lane);
-        }
-      }
-      float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-      if constexpr (F8) {
-#pragma unroll
-        for (int nb = 0; nb < 2; ++nb)
-#pragma unroll
-          for (int g = 0; g < D / 64; ++g) {
-            uint32_t w[4];
-            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                         : "r"(st + chunk8<D>(warp * 16 + nb * 8 + (lane >> 2), 4 * g + (lane & 3))));
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              mma16816<M>(sc[nb], qf[4 * g + i], e4m3_to_h2(w[i]), e4m3_to_h2_hi(w[i]));
+      for (int j = 0; j < D / 16; ++j) {
+        qf[nb][j][0] = qf[nb][j][1] = 0u;
+        if (row < G) {
+          const uint16_t* q0 = gq + (long)row * D + 16 * j;
+          if constexpr (F8) {
+            const uint2 w = *reinterpret_cast<const uint2*>(q0 + 4 * c);
+            qf[nb][j][0] = w.x;
+            qf[nb][j][1] = w.y;
+          } else {
+            qf[nb][j][0] = *reinterpret_cast<const uint32_t*>(q0 + 2 * c);
+            qf[nb][j][1] = *reinterpret_cast<const uint32_t*>(q0 + 8 + 2 * c);
           }
-      } else {
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          uint32_t bb[4];
-          frag_b_nk<kTileN>(bb, st, warp * 16, kk * 16, lane);
-          mma16816<M>(sc[0], qf[kk], bb[0], bb[1]);
-          mma16816<M>(sc[1], qf[kk], bb[2], bb[3]);
         }
       }
-      // scores in log2 units; this thread's keys are 8 nb + 2 (lane & 3) + {0, 1} of the warp's 16
-      float vsc[2][2] = {{1.f, 1.f}, {1.f, 1.f}};
-      const int key0 = lo + t * kTileN + warp * 16;
+      if constexpr (F8 && Elem<T>::kBf16) {
+        float amax = 0.f;
 #pragma unroll
-      for (int nb = 0; nb < 2; ++nb) {
-        float ks[2] = {1.f, 1.f};
-        if constexpr (F8) {
-          const int kc = warp * 16 + 8 * nb + 2 * (lane & 3);
-          const float* sp = reinterpret_cast<const float*>(smem + (st - sb) + 2 * L::kTile);
-          const float2 k2 = *reinterpret_cast<const float2*>(sp + kc);
-          const float2 v2 = *reinterpret_cast<const float2*>(sp + kTileN + kc);
-          ks[0] = k2.x;
-          ks[1] = k2.y;
-          vsc[nb][0] = v2.x;
-          vsc[nb][1] = v2.y;
-        }
+        for (int j = 0; j < D / 16; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          sc[nb][e] *= c[e >> 1] * ks[e & 1];
-          if (key0 + 8 * nb + 2 * (lane & 3) + (e & 1) >= hi) sc[nb][e] = -INFINITY;
-        }
+          for (int e = 0; e < 2; ++e) {
+            const float2 f = Elem<T>::unpack(qf[nb][j][e]);
+            amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+          }
+        amax = quad_max(amax);
+        // exponent of amax, kept where both powers of two are normal numbers
+        const int ex = min(max((int)(__float_as_uint(amax) >> 23) - 127, -100), 126);
+        mul = pow2(14 - ex);
+        unmul = pow2(ex - 14);
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float2 f = Elem<T>::unpack(qf[nb][j][e]);
+            qf[nb][j][e] = Elem<__half>::pack(f.x * mul, f.y * mul);
+          }
       }
-      float corr[2], mu[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        cq[nb][e] = p.scale * kLog2e * __shfl_sync(0xffffffffu, unmul, (2 * c + e) * 4);
+    }
+
+    // O^T: acc[nb][i] holds columns 16 i + .. of d (rows of the MMA) for query rows 2 c + {0, 1}
+    float acc[NB][D / 16][4];
+    float m[NB][2], l[NB][2];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) acc[nb][i][0] = acc[nb][i][1] = acc[nb][i][2] = acc[nb][i][3] = 0.f;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const float rm = fmaxf(fmaxf(sc[0][2 * e], sc[0][2 * e + 1]), fmaxf(sc[1][2 * e], sc[1][2 * e + 1]));
-        const float mnew = fmaxf(m_run[e], quad_max(rm));
-        mu[e] = (mnew == -INFINITY) ? 0.f : mnew;
-        corr[e] = ex2(m_run[e] - mu[e]);
-        m_run[e] = mnew;
-        l_run[e] *= corr[e];
+        m[nb][e] = -INFINITY;
+        l[nb][e] = 0.f;
       }
-      float vf[2][2] = {{1.f, 1.f}, {1.f, 1.f}};  // weight of p_j: s^v_j in units of 2^(ev - 14)
-      if constexpr (F8) {
-        const float vm = quad_max(fmaxf(fmaxf(vsc[0][0], vsc[0][1]), fmaxf(vsc[1][0], vsc[1][1])));
-        const int en = max((int)(__float_as_uint(fmaxf(vm, 0.f)) >> 23) - 126, ev);  // at most 129
-        if (en > ev) {  // the unit grows: O follows
-          const float down = ev - en < -126 ? 0.f : __uint_as_float((uint32_t)(ev - en + 127) << 23);
-          corr[0] *= down;
-          corr[1] *= down;
-          ev = en;
-        }
-        const float unit = __uint_as_float((uint32_t)(14 - ev + 127) << 23);
+    }
+    constexpr float kLift = !F8 && !Elem<T>::kBf16 ? 8.f : 0.f;  // fp16 weights of a 16-bit cache
+    int ev = kMinUnit;  // E4M3: 2^ev exceeds every V scale of this warp's keys so far
+
+    for (int i = 0; i < nblk; ++i) {
+      cp_async_wait<R::kStages - 2>();
+      __syncwarp();  // block i is there, and every lane is done with block i - 1
+      if (i + R::kStages - 1 < nblk) load(i + R::kStages - 1);
+      cp_async_commit();
+      const uint32_t st = ring + (i % R::kStages) * R::kStage;
+      const int key0 = first + i * 4 * R::kStep;
+
+      float sc[MB][NB][4];  // keys 16 mb + lane / 4 + {0, 8}, rows 8 nb + 2 c + {0, 1}
 #pragma unroll
-        for (int nb = 0; nb < 2; ++nb) {
-          vf[nb][0] = vsc[nb][0] * unit;
-          vf[nb][1] = vsc[nb][1] * unit;
-        }
-      }
-      uint32_t pa[4];
+      for (int mb = 0; mb < MB; ++mb) {
 #pragma unroll
-      for (int nb = 0; nb < 2; ++nb) {
-        const float p0 = ex2(sc[nb][0] - mu[0]), p1 = ex2(sc[nb][1] - mu[0]);
-        const float p2 = ex2(sc[nb][2] - mu[1]), p3 = ex2(sc[nb][3] - mu[1]);
-        l_run[0] += p0 + p1;
-        l_run[1] += p2 + p3;
-        pa[nb * 2 + 0] = Elem<M>::pack(p0 * vf[nb][0], p1 * vf[nb][1]);
-        pa[nb * 2 + 1] = Elem<M>::pack(p2 * vf[nb][0], p3 * vf[nb][1]);
-      }
+        for (int nb = 0; nb < NB; ++nb) sc[mb][nb][0] = sc[mb][nb][1] = sc[mb][nb][2] = sc[mb][nb][3] = 0.f;
+        if constexpr (F8) {
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i)
+          for (int j = 0; j < D / 16; j += 2) {
+            uint32_t r[4];
+            ldsm_x4(st + chunk_at<R::kRow>(16 * mb + (lane & 15), j + (lane >> 4)), r[0], r[1], r[2], r[3]);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][e] *= corr[e >> 1];
-      if constexpr (F8) {
-        // matrices of one ldmatrix.x4: keys 0-7 and 8-15 of 16-byte chunks 2 np and 2 np + 1
+            for (int h = 0; h < 2; ++h) {
+              uint32_t a[4];
+              e4m3x4_to_h2(r[2 * h], a[0], a[2]);
+              e4m3x4_to_h2(r[2 * h + 1], a[1], a[3]);
 #pragma unroll
-        for (int np = 0; np < D / 32; ++np) {
-          uint32_t r[4];
-          const int row = warp * 16 + (lane & 15);
-          ldsm_x4_t(st + L::kTile + chunk8<D>(row, 2 * np + (lane >> 4)), r[0], r[1], r[2], r[3]);
+              for (int nb = 0; nb < NB; ++nb) mma16816<M>(sc[mb][nb], a, qf[nb][j + h][0], qf[nb][j + h][1]);
+            }
+          }
+        } else {
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {  // chunk 2 np + k: columns 16 (2 np + k) + {even, odd}
-            const uint32_t a = __byte_perm(r[2 * k], 0, 0x3120), bq = __byte_perm(r[2 * k + 1], 0, 0x3120);
-            mma16816<M>(acc[4 * np + 2 * k], pa, e4m3_to_h2(a), e4m3_to_h2(bq));
-            mma16816<M>(acc[4 * np + 2 * k + 1], pa, e4m3_to_h2_hi(a), e4m3_to_h2_hi(bq));
+          for (int j = 0; j < D / 16; ++j) {
+            uint32_t a[4];
+            ldsm_x4(st + chunk_at<R::kRow>(16 * mb + (lane & 15), 2 * j + (lane >> 4)), a[0], a[1], a[2], a[3]);
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) mma16816<M>(sc[mb][nb], a, qf[nb][j][0], qf[nb][j][1]);
           }
         }
-      } else {
+      }
+      float vs[MB][2];
+      float vmax = 0.f;
 #pragma unroll
-        for (int np = 0; np < D / 16; ++np) {
-          uint32_t bb[4];
-          frag_b_kn<kTileN>(bb, st + L::kTile, warp * 16, np * 16, lane);
-          mma16816<M>(acc[2 * np], pa, bb[0], bb[1]);
-          mma16816<M>(acc[2 * np + 1], pa, bb[2], bb[3]);
+      for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float ks = 1.f;
+          vs[mb][e] = 1.f;
+          if constexpr (F8) {
+            const float* sp =
+                reinterpret_cast<const float*>(ring_g + (st - ring) + 2 * R::kTile) + 16 * mb + 8 * e + (lane >> 2);
+            ks = sp[0];
+            vs[mb][e] = sp[R::kStep];
+            vmax = fmaxf(vmax, vs[mb][e]);
+          }
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            sc[mb][nb][2 * e] *= cq[nb][0] * ks;
+            sc[mb][nb][2 * e + 1] *= cq[nb][1] * ks;
+          }
+        }
+      if (key0 + R::kStep > hi) {
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            if (key0 + 16 * mb + 8 * e + (lane >> 2) >= hi) {
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb) sc[mb][nb][2 * e] = sc[mb][nb][2 * e + 1] = -INFINITY;
+            }
+      }
+      float mx[NB][2];
+      bool grow = F8 && vmax >= pow2(ev);
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          mx[nb][e] = fmaxf(sc[0][nb][e], sc[0][nb][2 + e]);
+#pragma unroll
+          for (int mb = 1; mb < MB; ++mb) mx[nb][e] = fmaxf(mx[nb][e], fmaxf(sc[mb][nb][e], sc[mb][nb][2 + e]));
+          grow = grow || mx[nb][e] > m[nb][e] + kStale;
+        }
+      if (__any_sync(0xffffffffu, grow)) {
+        float down = 1.f;
+        if constexpr (F8) {  // the weights' unit grows: O follows
+          const int en = max((int)(__float_as_uint(rows_max(vmax)) >> 23) - 126, ev);  // at most 129
+          down = ev - en < -126 ? 0.f : pow2(ev - en);
+          ev = en;
+        }
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          float corr[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float mn = fmaxf(m[nb][e], rows_max(mx[nb][e]));
+            corr[e] = m[nb][e] == -INFINITY ? 0.f : ex2(m[nb][e] - mn);
+            m[nb][e] = mn;
+            l[nb][e] *= corr[e];
+            corr[e] *= down;
+          }
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[nb][k][e] *= corr[e & 1];
         }
       }
-      __syncthreads();
+      uint32_t pb[MB][NB][2];  // P^T as B fragments
+#pragma unroll
+      for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float vf = F8 ? vs[mb][e] * pow2(8 - ev) : 1.f;
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            const float mu0 = m[nb][0] == -INFINITY ? 0.f : m[nb][0] - kLift;
+            const float mu1 = m[nb][1] == -INFINITY ? 0.f : m[nb][1] - kLift;
+            const float p0 = ex2(sc[mb][nb][2 * e] - mu0), p1 = ex2(sc[mb][nb][2 * e + 1] - mu1);
+            l[nb][0] += p0;
+            l[nb][1] += p1;
+            pb[mb][nb][e] = transpose8(Elem<M>::pack(F8 ? p0 * vf : p0, F8 ? p1 * vf : p1));
+          }
+        }
+#pragma unroll
+      for (int mb = 0; mb < MB; ++mb) {
+        if constexpr (F8) {
+#pragma unroll
+          for (int k = 0; k < D / 16; k += 2) {
+            uint32_t r[4];  // keys 0-7 and 8-15 of 16-byte chunks k and k + 1
+            ldsm_x4_t(st + R::kTile + chunk_at<R::kRow>(16 * mb + (lane & 15), k + (lane >> 4)), r[0], r[1], r[2], r[3]);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t a[4];
+              e4m3x4_to_h2(__byte_perm(r[2 * h], 0, 0x3120), a[0], a[1]);
+              e4m3x4_to_h2(__byte_perm(r[2 * h + 1], 0, 0x3120), a[2], a[3]);
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb) mma16816<M>(acc[nb][k + h], a, pb[mb][nb][0], pb[mb][nb][1]);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            uint32_t a[4];  // (keys, columns) halves in the order (0, 0), (0, 8), (8, 0), (8, 8)
+            ldsm_x4_t(st + R::kTile + chunk_at<R::kRow>(16 * mb + (lane & 7) + 8 * (lane >> 4), 2 * k + ((lane >> 3) & 1)),
+                      a[0], a[1], a[2], a[3]);
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) mma16816<M>(acc[nb][k], a, pb[mb][nb][0], pb[mb][nb][1]);
+          }
+        }
+      }
     }
     cp_async_wait<0>();
     __syncthreads();
 
-    // merge the four warps: per warp m[16], l[16], O[16][D] (fp32) in the stage buffers
-    float* red_o = reinterpret_cast<float*>(smem + L::kOffStage);  // [4][16][D]
-    float* red_m = red_o + 4 * kRows * D;                          // [4][16]
-    float* red_l = red_m + 4 * kRows;                              // [4][16]
-    const int r0 = lane >> 2;
-    const float back = F8 ? __uint_as_float((uint32_t)(ev - 14 + 127) << 23) : 1.f;
+    // merge the four warps through shared memory: O [4][8 NB][D], m and l [4][8 NB], fp32
+    float* red_o = reinterpret_cast<float*>(smem);
+    float* red_m = red_o + 4 * 8 * NB * D;
+    float* red_l = red_m + 4 * 8 * NB;
+    const float back = F8 ? pow2(ev - 8) : 1.f;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const float l = quad_sum(l_run[e]);
-      if ((lane & 3) == 0) {
-        red_m[warp * kRows + r0 + 8 * e] = m_run[e];
-        red_l[warp * kRows + r0 + 8 * e] = l;
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int row = warp * 8 * NB + 8 * nb + 2 * (lane & 3) + e;
+        const float ls = rows_sum(l[nb][e]);
+        if (lane < 4) {
+          red_m[row] = m[nb][e];
+          red_l[row] = ls;
+        }
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          // MMA rows lane / 4 and lane / 4 + 8
+          const int c0 = 16 * k + (F8 ? 2 * (lane >> 2) : (lane >> 2)), c1 = F8 ? c0 + 1 : c0 + 8;
+          red_o[row * D + c0] = acc[nb][k][e] * back;
+          red_o[row * D + c1] = acc[nb][k][2 + e] * back;
+        }
       }
-    }
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i) {
-      // E4M3: block i holds the even (odd) columns of 16-byte chunk i / 2
-      const int c0 = F8 ? 16 * (i >> 1) + (i & 1) + 4 * (lane & 3) : 8 * i + 2 * (lane & 3);
-      const int c1 = F8 ? c0 + 2 : c0 + 1;
-      float* o0 = red_o + (warp * kRows + r0) * D;
-      float* o1 = red_o + (warp * kRows + r0 + 8) * D;
-      o0[c0] = acc[i][0] * back;
-      o0[c1] = acc[i][1] * back;
-      o1[c0] = acc[i][2] * back;
-      o1[c1] = acc[i][3] * back;
-    }
     __syncthreads();
     const long nparts = (long)p.B * p.Hq * S;
     const long part0 = ((long)b * p.Hq + (long)hk * G) * S + p.prefix_splits + s;
@@ -361,19 +420,20 @@ __global__ void __launch_bounds__(kThreads) cache_decode_kernel(CacheDecodeArgs 
       const int g = idx / D, col = idx % D;
       float mx = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < 4; ++w) mx = fmaxf(mx, red_m[w * kRows + g]);
+      for (int w = 0; w < 4; ++w) mx = fmaxf(mx, red_m[w * 8 * NB + g]);
       const float mu = mx == -INFINITY ? 0.f : mx;  // every score -inf (l = 0) or NaN (l NaN)
-      float l = 0.f, o = 0.f;
+      float lt = 0.f, o = 0.f;
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
-        const float f = ex2(red_m[w * kRows + g] - mu);
-        l += red_l[w * kRows + g] * f;
-        o += red_o[(w * kRows + g) * D + col] * f;
+        // a warp with no finite score has l and O of 0 or NaN in any unit
+        const float f = red_m[w * 8 * NB + g] == -INFINITY ? 1.f : ex2(red_m[w * 8 * NB + g] - mu);
+        lt += red_l[w * 8 * NB + g] * f;
+        o += red_o[(w * 8 * NB + g) * D + col] * f;
       }
       const long oi = part0 + (long)g * S;
       if (FA_IN_BOUNDS(p.status, oi, nparts)) {
-        p.o_part[oi * D + col] = l == 0.f ? 0.f : o / l;
-        if (col == 0) p.lse_part[oi] = (mu + log2f(l)) * kLn2;
+        p.o_part[oi * D + col] = lt == 0.f ? 0.f : o / lt;
+        if (col == 0) p.lse_part[oi] = (mu - (mx == -INFINITY ? 0.f : kLift) + log2f(lt)) * kLn2;
       }
     }
   }
@@ -383,51 +443,60 @@ __global__ void __launch_bounds__(kThreads) cache_decode_kernel(CacheDecodeArgs 
   if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-// Merge: one CTA per (h_q, b), its four warps each over a quarter of the live splits.
+// Merge: one CTA per (h_q, b).  Every warp first takes all live splits' LSE (one lane each, 32 at a
+// time) to the shared maximum, then sums its quarter of the splits, whose loads do not depend on one
+// another.
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) cache_combine_kernel(CacheDecodeArgs p) {
   __shared__ float red[4][D];
-  __shared__ float red_m[4], red_l[4];
+  __shared__ float red_l[4];
   const int h = blockIdx.x, b = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int S = p.prefix_splits + p.num_splits;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   int n = p.seqlens[b];
   n = n < 0 ? 0 : (n > p.Nk_max ? p.Nk_max : n);
   const int live = p.prefix_splits + (n + p.chunk - 1) / p.chunk;
   const long base = ((long)b * p.Hq + h) * S;
-  float m = -INFINITY, l = 0.f, o[D / 32];
+  const bool ok = FA_IN_BOUNDS(p.status, base + S - 1, (long)p.B * p.Hq * S);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  float mx = -INFINITY;
+  for (int s = lane; ok && s < live; s += 32) mx = fmaxf(mx, p.lse_part[base + s]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  const float mu = mx == -INFINITY ? 0.f : mx;
+  float l = 0.f;
+  float o[D / 32];
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) o[i] = 0.f;
-  if (FA_IN_BOUNDS(p.status, base + S - 1, (long)p.B * p.Hq * S)) {
+  if (ok) {
+#pragma unroll 4
     for (int s = warp; s < live; s += 4) {
-      const float x = p.lse_part[base + s] * kLog2e;
-      const float mn = fmaxf(m, x);
-      const float mu = mn == -INFINITY ? 0.f : mn;
-      const float corr = ex2(m - mu), w = ex2(x - mu);
-      m = mn;
-      l = l * corr + w;
+      const float w = ex2((p.lse_part[base + s] - mu) * kLog2e);
+      const float* row = p.o_part + (base + s) * D + lane * (D / 32);
+      float x[D / 32];
+      if constexpr (D == 128) {
+        const float4 f = *reinterpret_cast<const float4*>(row);
+        x[0] = f.x;
+        x[1] = f.y;
+        x[2] = f.z;
+        x[3] = f.w;
+      } else {
+        const float2 f = *reinterpret_cast<const float2*>(row);
+        x[0] = f.x;
+        x[1] = f.y;
+      }
+      l += w;
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) o[i] = o[i] * corr + w * p.o_part[(base + s) * D + i * 32 + lane];
+      for (int i = 0; i < D / 32; ++i) o[i] += w * x[i];
     }
   }
 #pragma unroll
-  for (int i = 0; i < D / 32; ++i) red[warp][i * 32 + lane] = o[i];
-  if (lane == 0) {
-    red_m[warp] = m;
-    red_l[warp] = l;
-  }
+  for (int i = 0; i < D / 32; ++i) red[warp][lane * (D / 32) + i] = o[i];
+  if (lane == 0) red_l[warp] = l;
   __syncthreads();
   const int col = threadIdx.x;
   if (col >= D) return;
-  const float mx = fmaxf(fmaxf(red_m[0], red_m[1]), fmaxf(red_m[2], red_m[3]));
-  const float mu = mx == -INFINITY ? 0.f : mx;
-  float lt = 0.f, ot = 0.f;
-#pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    const float f = ex2(red_m[w] - mu);
-    lt += red_l[w] * f;
-    ot += red[w][col] * f;
-  }
+  const float lt = (red_l[0] + red_l[1]) + (red_l[2] + red_l[3]);
+  const float ot = (red[0][col] + red[1][col]) + (red[2][col] + red[3][col]);
   const long row = (long)b * p.Hq + h;
   const float out = lt == 0.f ? 0.f : ot / lt;  // no key: O = 0, LSE = -inf
   uint16_t* go = static_cast<uint16_t*>(p.o) + row * D;
@@ -435,14 +504,14 @@ __global__ void __launch_bounds__(kThreads) cache_combine_kernel(CacheDecodeArgs
   if constexpr (Elem<T>::kBf16) v = __float2bfloat16_rn(out); else v = __float2half_rn(out);
   if (FA_IN_BOUNDS(p.status, row, (long)p.B * p.Hq)) {
     go[col] = *reinterpret_cast<uint16_t*>(&v);
-    if (col == 0) p.lse[row] = (mu + log2f(lt)) * kLn2;
+    if (col == 0) p.lse[row] = mu + logf(lt);
   }
 }
 
-template <typename T, int D, bool F8>
+template <typename T, int D, bool F8, int NB>
 cudaError_t launch_part(const CacheDecodeArgs& a, int after_prefix, cudaStream_t s) {
-  auto kern = cache_decode_kernel<T, D, F8>;
-  constexpr int smem = Smem<T, D, F8>::kBytes;
+  auto kern = cache_decode_kernel<T, D, F8, NB>;
+  constexpr int smem = Smem<D, F8, NB>::kBytes;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
@@ -462,7 +531,9 @@ cudaError_t launch_part(const CacheDecodeArgs& a, int after_prefix, cudaStream_t
 
 template <typename T, int D>
 cudaError_t launch_part_d(const CacheDecodeArgs& a, int after_prefix, cudaStream_t s) {
-  return a.k_scale ? launch_part<T, D, true>(a, after_prefix, s) : launch_part<T, D, false>(a, after_prefix, s);
+  const bool wide = a.Hq / a.Hkv > 8;  // groups of 9 to 16 query heads take two column blocks
+  if (a.k_scale) return wide ? launch_part<T, D, true, 2>(a, after_prefix, s) : launch_part<T, D, true, 1>(a, after_prefix, s);
+  return wide ? launch_part<T, D, false, 2>(a, after_prefix, s) : launch_part<T, D, false, 1>(a, after_prefix, s);
 }
 
 template <typename T, int D>

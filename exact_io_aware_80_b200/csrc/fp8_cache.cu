@@ -36,9 +36,80 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
-// One row in D / 16 consecutive threads, 16 values each.
+// Row r = (b n + i) Hkv + h of the 16-bit tensors.
+struct Rows {
+  uint32_t count;  // < 2^31
+  FastDiv n, Hkv;
+};
+struct Row {
+  uint32_t b, i, h;
+};
+__device__ __forceinline__ Row row_at(const Rows& rows, uint32_t r) {
+  const uint32_t bi = rows.Hkv(r), b = rows.n(bi);
+  return Row{b, bi - b * rows.n.d, r - bi * rows.Hkv.d};
+}
+
+// E4M3 codes of 16 values x / s.  For 2^-90 <= s <= 2^90 a quotient is y = x r with r = RN(1 / s),
+// corrected once by its own remainder: q = y + (x - y s) r, which is RN(x / s) as long as nothing
+// leaves the normal range (Markstein, "Computation of elementary functions on the IBM RISC
+// System/6000 processor", 1990).  Quotients small enough to leave it have the code +-0 either way;
+// -0 alone loses its sign in the correction and takes y's.  Other scales divide.
+template <bool FAST>
+__device__ __forceinline__ uint4 codes16(const float (&x)[16], float s) {
+  const float r = __frcp_rn(s);
+  uint32_t c[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t half[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const float2 v = make_float2(x[4 * i + 2 * k], x[4 * i + 2 * k + 1]);
+      float2 q;
+      if constexpr (FAST) {
+        const float2 y = __fmul2_rn(v, make_float2(r, r));
+        const float2 rem = __ffma2_rn(y, make_float2(-s, -s), v);
+        q = __ffma2_rn(rem, make_float2(r, r), y);
+        q.x = __uint_as_float(__float_as_uint(q.x) | (__float_as_uint(y.x) & 0x80000000u));
+        q.y = __uint_as_float(__float_as_uint(q.y) | (__float_as_uint(y.y) & 0x80000000u));
+      } else {
+        q = make_float2(__fdiv_rn(v.x, s), __fdiv_rn(v.y, s));
+      }
+      half[k] = e4m3x2(q.x, q.y);
+    }
+    c[i] = half[0] | (half[1] << 16);
+  }
+  return make_uint4(c[0], c[1], c[2], c[3]);
+}
+
+// grid: (row groups, 2); y = 0 appends K rows, 1 V rows.  D / 16 consecutive threads hold a row.
 template <typename T, int D>
-__device__ __forceinline__ void encode(const uint4 (&w)[2], uint8_t* codes, float* scale, int unit) {
+__global__ void __launch_bounds__(kThreads) append_kernel(Fp8CacheArgs p, Rows rows) {
+  constexpr int kUnits = D / 16;
+  const bool isv = blockIdx.y != 0;
+  const uint32_t r = blockIdx.x * (kThreads / kUnits) + threadIdx.x / kUnits;
+  const int unit = threadIdx.x % kUnits;
+  uint8_t* codes = nullptr;
+  float* scale = nullptr;
+  uint4 w[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+  if (r < rows.count) {
+    const Row at = row_at(rows, r);
+    const long dst = (long)p.start[at.b] + at.i;
+    if ((int)at.i < (p.counts ? p.counts[at.b] : p.n) && dst >= 0 && dst < p.Nk_max) {
+      const long bs = isv ? p.v_bs : p.k_bs, ts = isv ? p.v_ts : p.k_ts;
+      const long in = at.b * bs + at.i * ts + (long)(at.h * D);
+      const long crow = ((long)at.b * p.Nk_max + dst) * p.Hkv + at.h;
+      const long srow = ((long)at.b * p.Hkv + at.h) * p.Nk_max + dst;
+      if (FA_IN_BOUNDS(p.status, in + D - 1, (p.B - 1) * bs + (p.n - 1) * ts + (long)p.Hkv * D) &&
+          FA_IN_BOUNDS(p.status, crow, (long)p.B * p.Nk_max * p.Hkv) &&
+          FA_IN_BOUNDS(p.status, srow, (long)p.B * p.Nk_max * p.Hkv)) {
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(isv ? p.v : p.k) + in) + 2 * unit;
+        w[0] = src[0];
+        w[1] = src[1];
+        codes = (isv ? p.v8 : p.k8) + crow * D;
+        scale = (isv ? p.v_scale : p.k_scale) + srow;
+      }
+    }
+  }
   const uint32_t u[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
   float x[16];
 #pragma unroll
@@ -53,50 +124,11 @@ __device__ __forceinline__ void encode(const uint4 (&w)[2], uint8_t* codes, floa
 #pragma unroll
   for (int o = D / 32; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
   const float s = amax == 0.f ? 1.f : __fdiv_rn(amax, 448.f);
-  uint32_t c[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    c[i] = e4m3x2(__fdiv_rn(x[4 * i], s), __fdiv_rn(x[4 * i + 1], s)) |
-           (e4m3x2(__fdiv_rn(x[4 * i + 2], s), __fdiv_rn(x[4 * i + 3], s)) << 16);
   if (codes) {
-    *reinterpret_cast<uint4*>(codes + 16 * unit) = make_uint4(c[0], c[1], c[2], c[3]);
+    *reinterpret_cast<uint4*>(codes + 16 * unit) =
+        s >= 0x1p-90f && s <= 0x1p90f ? codes16<true>(x, s) : codes16<false>(x, s);
     if (unit == 0) *scale = s;
   }
-}
-
-// grid: (row groups, 2); y = 0 appends K rows, 1 V rows.  Row r = (b n + i) Hkv + h.
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) append_kernel(Fp8CacheArgs p) {
-  constexpr int kUnits = D / 16;
-  const bool isv = blockIdx.y != 0;
-  const long rows = (long)p.B * p.n * p.Hkv;
-  const long r = (long)blockIdx.x * (kThreads / kUnits) + threadIdx.x / kUnits;
-  const int unit = threadIdx.x % kUnits;
-  uint8_t* codes = nullptr;
-  float* scale = nullptr;
-  uint4 w[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-  if (r < rows) {
-    const int h = (int)(r % p.Hkv);
-    const long bi = r / p.Hkv;
-    const int i = (int)(bi % p.n), b = (int)(bi / p.n);
-    const long dst = (long)p.start[b] + i;
-    if (i < (p.counts ? p.counts[b] : p.n) && dst >= 0 && dst < p.Nk_max) {
-      const long bs = isv ? p.v_bs : p.k_bs, ts = isv ? p.v_ts : p.k_ts;
-      const long in = b * bs + i * ts + (long)h * D;
-      const long crow = ((long)b * p.Nk_max + dst) * p.Hkv + h;
-      const long srow = ((long)b * p.Hkv + h) * p.Nk_max + dst;
-      if (FA_IN_BOUNDS(p.status, in + D - 1, (p.B - 1) * bs + (p.n - 1) * ts + (long)p.Hkv * D) &&
-          FA_IN_BOUNDS(p.status, crow, (long)p.B * p.Nk_max * p.Hkv) &&
-          FA_IN_BOUNDS(p.status, srow, (long)p.B * p.Nk_max * p.Hkv)) {
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(isv ? p.v : p.k) + in) + 2 * unit;
-        w[0] = src[0];
-        w[1] = src[1];
-        codes = (isv ? p.v8 : p.k8) + crow * D;
-        scale = (isv ? p.v_scale : p.k_scale) + srow;
-      }
-    }
-  }
-  encode<T, D>(w, codes, scale, unit);
 }
 
 // 16 E4M3 codes times s, as two 16-byte vectors of T.
@@ -118,46 +150,63 @@ __device__ __forceinline__ void decode16(const uint4 c, float s, uint4 (&out)[2]
   out[1] = make_uint4(w[4], w[5], w[6], w[7]);
 }
 
-// grid: (row groups, 2).  Rows at or past a sequence's length come out as zeros.
+// grid: (row groups, 2).  Rows at or past a sequence's length come out as zeros.  A thread takes 16
+// codes of kReadRows rows, whose loads it issues together.
+constexpr int kReadRows = 2;
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) read_kernel(Fp8CacheArgs p) {
-  constexpr int kUnits = D / 16;
+__global__ void __launch_bounds__(kThreads) read_kernel(Fp8CacheArgs p, Rows rows) {
+  constexpr int kUnits = D / 16, kPer = kThreads / kUnits;
   const bool isv = blockIdx.y != 0;
-  const long rows = (long)p.B * p.n * p.Hkv;
-  const long r = (long)blockIdx.x * (kThreads / kUnits) + threadIdx.x / kUnits;
+  const uint32_t r0 = blockIdx.x * (kPer * kReadRows) + threadIdx.x / kUnits;
   const int unit = threadIdx.x % kUnits;
-  if (r >= rows) return;
-  const int h = (int)(r % p.Hkv);
-  const long bi = r / p.Hkv;
-  const int i = (int)(bi % p.n), b = (int)(bi / p.n);
-  uint4 w[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-  if (i < p.counts[b]) {
-    const long crow = ((long)b * p.Nk_max + i) * p.Hkv + h;
-    const long srow = ((long)b * p.Hkv + h) * p.Nk_max + i;
-    if (FA_IN_BOUNDS(p.status, crow, (long)p.B * p.Nk_max * p.Hkv) &&
-        FA_IN_BOUNDS(p.status, srow, (long)p.B * p.Nk_max * p.Hkv))
-      decode16<T>(reinterpret_cast<const uint4*>((isv ? p.v8 : p.k8) + crow * D)[unit],
-                  (isv ? p.v_scale : p.k_scale)[srow], w);
+  uint4 c[kReadRows];
+  float s[kReadRows];
+  bool live[kReadRows];
+#pragma unroll
+  for (int k = 0; k < kReadRows; ++k) {
+    const uint32_t r = r0 + k * kPer;
+    live[k] = false;
+    if (r < rows.count) {
+      const Row at = row_at(rows, r);
+      if ((int)at.i < p.counts[at.b]) {
+        const long crow = ((long)at.b * p.Nk_max + at.i) * p.Hkv + at.h;
+        const long srow = ((long)at.b * p.Hkv + at.h) * p.Nk_max + at.i;
+        if (FA_IN_BOUNDS(p.status, crow, (long)p.B * p.Nk_max * p.Hkv) &&
+            FA_IN_BOUNDS(p.status, srow, (long)p.B * p.Nk_max * p.Hkv)) {
+          live[k] = true;
+          c[k] = reinterpret_cast<const uint4*>((isv ? p.v8 : p.k8) + crow * D)[unit];
+          s[k] = (isv ? p.v_scale : p.k_scale)[srow];
+        }
+      }
+    }
   }
-  if (FA_IN_BOUNDS(p.status, r, rows)) {
-    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(isv ? p.v_out : p.k_out) + r * D) + 2 * unit;
-    dst[0] = w[0];
-    dst[1] = w[1];
+#pragma unroll
+  for (int k = 0; k < kReadRows; ++k) {
+    const uint32_t r = r0 + k * kPer;
+    if (r < rows.count && FA_IN_BOUNDS(p.status, r, rows.count)) {
+      uint4 w[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+      if (live[k]) decode16<T>(c[k], s[k], w);
+      uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(isv ? p.v_out : p.k_out) + (long)r * D) + 2 * unit;
+      dst[0] = w[0];
+      dst[1] = w[1];
+    }
   }
 }
 
+Rows rows_of(const Fp8CacheArgs& a) { return Rows{(uint32_t)a.B * a.n * a.Hkv, FastDiv(a.n), FastDiv(a.Hkv)}; }
+
 template <typename T, int D>
 cudaError_t launch_append(const Fp8CacheArgs& a, cudaStream_t s) {
-  const long rows = (long)a.B * a.n * a.Hkv, per = kThreads / (D / 16), groups = (rows + per - 1) / per;
-  if (groups > 0x7fffffffL) return cudaErrorInvalidValue;
-  append_kernel<T, D><<<dim3((unsigned)groups, 2), kThreads, 0, s>>>(a);
+  const Rows rows = rows_of(a);
+  const uint32_t per = kThreads / (D / 16);
+  append_kernel<T, D><<<dim3((rows.count + per - 1) / per, 2), kThreads, 0, s>>>(a, rows);
   return cudaGetLastError();
 }
 template <typename T, int D>
 cudaError_t launch_read(const Fp8CacheArgs& a, cudaStream_t s) {
-  const long rows = (long)a.B * a.n * a.Hkv, per = kThreads / (D / 16), groups = (rows + per - 1) / per;
-  if (groups > 0x7fffffffL) return cudaErrorInvalidValue;
-  read_kernel<T, D><<<dim3((unsigned)groups, 2), kThreads, 0, s>>>(a);
+  const Rows rows = rows_of(a);
+  const uint32_t per = kThreads / (D / 16) * kReadRows;
+  read_kernel<T, D><<<dim3((rows.count + per - 1) / per, 2), kThreads, 0, s>>>(a, rows);
   return cudaGetLastError();
 }
 

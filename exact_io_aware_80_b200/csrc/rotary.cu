@@ -17,11 +17,14 @@
 // Bound by HBM: every element is read and written once.  A thread takes 8
 // pairs of one token (two 16-byte chunks: chunks j and j + rot/16 of the head
 // in the half layout, 2j and 2j + 1 in the interleaved one), computes their
-// sines once, and applies them to up to kHeads heads, whose loads it issues
-// together.
+// sines once, and applies them to one head after another, kBatch heads' loads
+// at a time.
 #include <math.h>
 
+#include <algorithm>
+
 #include "common.cuh"
+#include "kernels.h"
 #include "serving.h"
 
 namespace fa {
@@ -34,8 +37,10 @@ struct Params {
   uint16_t *qo, *ko;
   const int* positions;
   const unsigned long long* turns;
-  long tokens;  // B N
-  int N, Hq, Hkv, rot;
+  uint32_t tokens;  // B N < 2^31
+  FastDiv N;
+  int Hq, Hkv, rot;
+  int per_y;  // heads per grid row
   long q_bs, q_ts, k_bs, k_ts, pos_stride;
   long q_len, k_len;  // elements from q (k) to the end of its last row
   float mag, sign;
@@ -58,110 +63,133 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
                     Elem<T>::pack(x[6], x[7]));
 }
 
+// The rotation of one thread's 8 pairs; cosines and sines as pairs of neighbouring j.
+template <typename T, bool INTER>
+__device__ __forceinline__ void turn(uint4& w0, uint4& w1, const float2 (&cs)[4], const float2 (&sn)[4]) {
+  float x[8], y[8];
+  load8<T>(x, w0);
+  load8<T>(y, w1);
+  float u[8], v[8];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    // pairs 2j and 2j + 1: (x[.], y[.]), or neighbours within the two chunks
+    float2 a, c;
+    if constexpr (INTER) {
+      const float* z = j < 2 ? x : y;
+      a = make_float2(z[4 * (j & 1)], z[4 * (j & 1) + 2]);
+      c = make_float2(z[4 * (j & 1) + 1], z[4 * (j & 1) + 3]);
+    } else {
+      a = make_float2(x[2 * j], x[2 * j + 1]);
+      c = make_float2(y[2 * j], y[2 * j + 1]);
+    }
+    const float2 ns = make_float2(-sn[j].x, -sn[j].y);
+    const float2 r0 = __ffma2_rn(a, cs[j], __fmul2_rn(c, ns));
+    const float2 r1 = __ffma2_rn(c, cs[j], __fmul2_rn(a, sn[j]));
+    u[2 * j] = r0.x;
+    u[2 * j + 1] = r0.y;
+    v[2 * j] = r1.x;
+    v[2 * j + 1] = r1.y;
+  }
+  if constexpr (INTER) {
+    w0 = make_uint4(Elem<T>::pack(u[0], v[0]), Elem<T>::pack(u[1], v[1]), Elem<T>::pack(u[2], v[2]),
+                    Elem<T>::pack(u[3], v[3]));
+    w1 = make_uint4(Elem<T>::pack(u[4], v[4]), Elem<T>::pack(u[5], v[5]), Elem<T>::pack(u[6], v[6]),
+                    Elem<T>::pack(u[7], v[7]));
+  } else {
+    w0 = pack8<T>(u);
+    w1 = pack8<T>(v);
+  }
+}
+
 // grid: (token groups, head groups); a warp covers 32 / (D / 16) heads of one token at a time.
-template <typename T, int D, bool INTER, int HEADS>
+template <typename T, int D, bool INTER, int BATCH>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(Params p) {
-  constexpr int kUnits = D / 16;         // threads per head, 16 values each
-  constexpr int kRow = 32 / kUnits;      // heads per warp and step
+  constexpr int kUnits = D / 16;     // threads per head, 16 values each
+  constexpr int kRow = 32 / kUnits;  // heads per warp and step
   const int lane = threadIdx.x & 31;
-  const long tok = (long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  const uint32_t tok = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
   if (tok >= p.tokens) return;
   const int unit = lane % kUnits;
-  const int h0 = blockIdx.y * (kRow * HEADS) + lane / kUnits;
   const int H = p.Hq + p.Hkv;
-  const long b = tok / p.N, n = tok % p.N;
-  const int units_rot = p.rot / 16;
-  const bool turned = unit < units_rot;
+  const uint32_t b = p.N(tok), n = tok - b * p.N.d;
+  const bool turned = unit < p.rot / 16;
   // first and second 8-value chunk of this thread within a head
   const int c0 = INTER || !turned ? 16 * unit : 8 * unit;
   const int c1 = INTER || !turned ? 16 * unit + 8 : p.rot / 2 + 8 * unit;
+  const long q_in = b * p.q_bs + n * p.q_ts, k_in = b * p.k_bs + n * p.k_ts;
+  const long q_out = (long)tok * p.Hq * D, k_out = (long)tok * p.Hkv * D;
+  const int h_end = min(H, (int)(blockIdx.y + 1) * p.per_y);
 
-  const uint16_t* src[HEADS];
-  uint16_t* dst[HEADS];
-  uint4 w0[HEADS], w1[HEADS];
+  float2 cs[4], sn[4];
+  bool have = false;
+  for (int h0 = blockIdx.y * p.per_y + lane / kUnits; h0 < h_end; h0 += kRow * BATCH) {
+    uint4 w0[BATCH], w1[BATCH];
+    uint16_t* dst[BATCH];
 #pragma unroll
-  for (int i = 0; i < HEADS; ++i) {
-    const int h = h0 + i * kRow;
-    const bool isq = h < p.Hq;
-    const long in = isq ? b * p.q_bs + n * p.q_ts + (long)h * D : b * p.k_bs + n * p.k_ts + (long)(h - p.Hq) * D;
-    const long out = (isq ? tok * p.Hq + h : tok * p.Hkv + (h - p.Hq)) * D;
-    bool ok = h < H;
-    ok = ok && FA_IN_BOUNDS(p.status, in + D - 1, isq ? p.q_len : p.k_len) &&
-         FA_IN_BOUNDS(p.status, out + D - 1, p.tokens * (isq ? p.Hq : p.Hkv) * D);
-    src[i] = ok ? (isq ? p.q : p.k) + in : nullptr;
-    dst[i] = (isq ? p.qo : p.ko) + out;
-    if (src[i]) {
-      w0[i] = *reinterpret_cast<const uint4*>(src[i] + c0);
-      w1[i] = *reinterpret_cast<const uint4*>(src[i] + c1);
+    for (int i = 0; i < BATCH; ++i) {
+      const int h = h0 + i * kRow;
+      const bool isq = h < p.Hq;
+      const long in = isq ? q_in + h * D : k_in + (h - p.Hq) * D;
+      const long out = isq ? q_out + h * D : k_out + (h - p.Hq) * D;
+      const bool ok = h < h_end && FA_IN_BOUNDS(p.status, in + D - 1, isq ? p.q_len : p.k_len) &&
+                      FA_IN_BOUNDS(p.status, out + D - 1, (long)p.tokens * (isq ? p.Hq : p.Hkv) * D);
+      dst[i] = ok ? (isq ? p.qo : p.ko) + out : nullptr;
+      if (ok) {
+        const uint16_t* src = (isq ? p.q : p.k) + in;
+        w0[i] = *reinterpret_cast<const uint4*>(src + c0);
+        w1[i] = *reinterpret_cast<const uint4*>(src + c1);
+      }
     }
-  }
-  if (!turned) {
+    if (turned && !have) {  // while the first batch is in flight
+      have = true;
+      const long long pos = p.positions[b * p.pos_stride + n];
+      auto angle = [&](int j, float* sine, float* cosine) {
+        const unsigned long long phase = (unsigned long long)pos * p.turns[8 * unit + j];
+        sincospif((float)(int)(phase >> 32) * 0x1p-31f, sine, cosine);  // half turns in [-1, 1]
+        *sine *= p.sign * p.mag;
+        *cosine *= p.mag;
+      };
 #pragma unroll
-    for (int i = 0; i < HEADS; ++i)
-      if (src[i]) {
+      for (int j = 0; j < 4; ++j) {
+        angle(2 * j, &sn[j].x, &cs[j].x);
+        angle(2 * j + 1, &sn[j].y, &cs[j].y);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i)
+      if (dst[i]) {
+        if (turned) turn<T, INTER>(w0[i], w1[i], cs, sn);
         *reinterpret_cast<uint4*>(dst[i] + c0) = w0[i];
         *reinterpret_cast<uint4*>(dst[i] + c1) = w1[i];
       }
-    return;
   }
-  const long long pos = p.positions[b * p.pos_stride + n];
-  float cs[8], sn[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const unsigned long long phase = (unsigned long long)pos * p.turns[8 * unit + j];
-    const float half_turns = (float)(int)(phase >> 32) * 0x1p-31f;  // in [-1, 1]
-    sincospif(half_turns, &sn[j], &cs[j]);
-    sn[j] *= p.sign * p.mag;
-    cs[j] *= p.mag;
-  }
-#pragma unroll
-  for (int i = 0; i < HEADS; ++i)
-    if (src[i]) {
-      float x[8], y[8], u[8], v[8];
-      load8<T>(x, w0[i]);
-      load8<T>(y, w1[i]);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        // pair j: (x[j], y[j]), or neighbours within the two chunks
-        const float a = INTER ? (j < 4 ? x[(2 * j) & 7] : y[(2 * j) & 7]) : x[j];
-        const float c = INTER ? (j < 4 ? x[(2 * j + 1) & 7] : y[(2 * j + 1) & 7]) : y[j];
-        u[j] = fmaf(a, cs[j], -c * sn[j]);
-        v[j] = fmaf(c, cs[j], a * sn[j]);
-      }
-      if constexpr (INTER) {
-        *reinterpret_cast<uint4*>(dst[i] + c0) =
-            make_uint4(Elem<T>::pack(u[0], v[0]), Elem<T>::pack(u[1], v[1]), Elem<T>::pack(u[2], v[2]),
-                       Elem<T>::pack(u[3], v[3]));
-        *reinterpret_cast<uint4*>(dst[i] + c1) =
-            make_uint4(Elem<T>::pack(u[4], v[4]), Elem<T>::pack(u[5], v[5]), Elem<T>::pack(u[6], v[6]),
-                       Elem<T>::pack(u[7], v[7]));
-      } else {
-        *reinterpret_cast<uint4*>(dst[i] + c0) = pack8<T>(u);
-        *reinterpret_cast<uint4*>(dst[i] + c1) = pack8<T>(v);
-      }
-    }
 }
 
-template <typename T, int D, bool INTER, int HEADS>
-cudaError_t launch(const Params& p, cudaStream_t s) {
-  constexpr int kRow = 32 / (D / 16);
-  const long groups = (p.tokens + kThreads / 32 - 1) / (kThreads / 32);
-  if (groups > 0x7fffffffL) return cudaErrorInvalidValue;
-  dim3 grid((unsigned)groups, (p.Hq + p.Hkv + kRow * HEADS - 1) / (kRow * HEADS));
-  rotary_kernel<T, D, INTER, HEADS><<<grid, kThreads, 0, s>>>(p);
+template <typename T, int D, bool INTER>
+cudaError_t launch(const RotaryArgs& a, Params p, cudaStream_t s) {
+  constexpr int kRow = 32 / (D / 16), kBatch = 2;
+  const unsigned groups = (p.tokens + kThreads / 32 - 1) / (kThreads / 32);
+  const int H = a.Hq + a.Hkv;
+  // a warp takes all heads of its token, or fewer where there are too few tokens to fill the SMs
+  const int steps = (H + kRow * kBatch - 1) / (kRow * kBatch);
+  const long want = 16l * device_sm_count();  // thread blocks
+  const int rows = (int)std::min<long>(steps, std::max<long>(1, want / groups));
+  p.per_y = (steps + rows - 1) / rows * (kRow * kBatch);
+  const dim3 grid(groups, (H + p.per_y - 1) / p.per_y);
+  rotary_kernel<T, D, INTER, kBatch><<<grid, kThreads, 0, s>>>(p);
   return cudaGetLastError();
 }
 
 template <typename T, int D>
 cudaError_t launch_d(const RotaryArgs& a, const Params& p, cudaStream_t s) {
-  return a.interleaved ? launch<T, D, true, 2>(p, s) : launch<T, D, false, 2>(p, s);
+  return a.interleaved ? launch<T, D, true>(a, p, s) : launch<T, D, false>(a, p, s);
 }
 
 }  // namespace
 
 cudaError_t launch_rotary(const RotaryArgs& a, cudaStream_t s) {
   Params p{static_cast<const uint16_t*>(a.q), static_cast<const uint16_t*>(a.k), static_cast<uint16_t*>(a.q_out),
-           static_cast<uint16_t*>(a.k_out), a.positions, a.turns, (long)a.B * a.N, a.N, a.Hq, a.Hkv, a.rot,
+           static_cast<uint16_t*>(a.k_out), a.positions, a.turns, (uint32_t)a.B * a.N, FastDiv(a.N), a.Hq, a.Hkv, a.rot, 0,
            a.q_bs, a.q_ts, a.k_bs, a.k_ts, a.pos_stride,
            (a.B - 1) * a.q_bs + (a.N - 1) * a.q_ts + (long)a.Hq * a.d,
            (a.B - 1) * a.k_bs + (a.N - 1) * a.k_ts + (long)a.Hkv * a.d, a.magnitude, a.inverse ? -1.f : 1.f, a.status};

@@ -18,6 +18,20 @@ constexpr int kMapF16 = 0, kMapBf16 = 1, kMapF32 = 2;
 bool make_map_box(CUtensorMap* m, const void* base, int type, const uint64_t dims[4], const uint64_t strides[3],
                   const uint32_t box[4]);
 
+// Division of n < 2^31 by a fixed d >= 1: with l = ceil(log2 d) and m = floor(2^32 (2^l - d) / d) + 1,
+// floor(n / d) = (mulhi(n, m) + n) >> l (Granlund and Montgomery, "Division by invariant integers
+// using multiplication", 1994; the sum stays below 2^32 for these n).
+struct FastDiv {
+  uint32_t d, m, l;
+  explicit FastDiv(uint32_t div = 1) : d(div), l(0) {
+    while ((1ull << l) < d) ++l;
+    m = (uint32_t)((((1ull << l) - d) << 32) / d + 1);
+  }
+#ifdef __CUDACC__
+  __device__ __forceinline__ uint32_t operator()(uint32_t n) const { return (__umulhi(n, m) + n) >> l; }
+#endif
+};
+
 // Rotary positions of q [B,N,Hq,d] and k [B,N,Hkv,d] (rotary.cu).  Input strides in elements
 // (heads are d apart); outputs contiguous, or the inputs themselves.
 struct RotaryArgs {

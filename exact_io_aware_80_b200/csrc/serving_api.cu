@@ -105,7 +105,7 @@ fa_status fa_fp8_cache_append(const void* k, const void* v, void* k8, void* v8, 
   if (dt != FA_FP16 && dt != FA_BF16) return FA_ERR_UNSUPPORTED;
   if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
   if (B > 65535 || Hkv > 65535 || Nk_max > (1 << 30)) return FA_ERR_UNSUPPORTED;
-  if ((long long)B * n > (1ll << 31) - 1) return FA_ERR_UNSUPPORTED;
+  if ((long long)B * n * Hkv > (1ll << 31) - 1) return FA_ERR_UNSUPPORTED;
   if (!aligned(k, 16) || !aligned(v, 16) || !aligned(k8, 16) || !aligned(v8, 16) || !aligned(k_scale, 4) ||
       !aligned(v_scale, 4) || !aligned(start, 4) || (counts && !aligned(counts, 4)) ||
       !strides_aligned(k_batch_stride, k_token_stride) || !strides_aligned(v_batch_stride, v_token_stride))
@@ -142,7 +142,7 @@ fa_status fa_fp8_cache_read(const void* k8, const void* v8, const float* k_scale
   if (dt != FA_FP16 && dt != FA_BF16) return FA_ERR_UNSUPPORTED;
   if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
   if (B > 65535 || Hkv > 65535 || Nk_max > (1 << 30)) return FA_ERR_UNSUPPORTED;
-  if ((long long)B * Nk > (1ll << 31) - 1) return FA_ERR_UNSUPPORTED;
+  if ((long long)B * Nk * Hkv > (1ll << 31) - 1) return FA_ERR_UNSUPPORTED;
   if (!aligned(k8, 16) || !aligned(v8, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(k_scale, 4) ||
       !aligned(v_scale, 4) || !aligned(seqlens_k, 4))
     return FA_ERR_ALIGN;

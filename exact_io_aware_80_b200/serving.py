@@ -11,6 +11,7 @@ seqlens_k, start, counts int32 [B].
 """
 from __future__ import annotations
 
+import functools
 import math
 
 from . import _lib
@@ -18,49 +19,68 @@ from . import _lib
 __all__ = ["rotary_table", "rotary_magnitude", "rotary_fwd", "rotary_bwd", "fp8_cache_append", "fp8_cache_read",
            "decode_fp8", "decode_shared_prefix"]
 
+# These calls serve single tokens, where the host's share of a pass is the larger one; checks
+# therefore pass on one expression and take a bad tensor apart only to say what is wrong with it.
+_modules = None
+
 
 def _torch():
-    import torch
-    return torch
+    global _modules
+    if _modules is None:
+        import torch
+        _modules = torch
+    return _modules
 
 
 def _dt(t):
     torch = _torch()
-    if t.dtype == torch.bfloat16:
+    if t.dtype is torch.bfloat16:
         return _lib.FA_BF16
-    if t.dtype == torch.float16:
+    if t.dtype is torch.float16:
         return _lib.FA_FP16
     raise TypeError(f"attention tensors must be fp16 or bf16, got {t.dtype}")
 
 
+def _device(t):
+    dev = t.device
+    if dev.type != "cuda":
+        raise ValueError("libfa.so takes CUDA tensors only (no CPU path)")
+    return dev
+
+
 def _check(name, t, dtype, shape, dev, contiguous=True):
-    if t.device != dev or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor on the device of the first argument (no CPU path)")
+    if t.dtype is dtype and t.shape == shape and t.device == dev and (not contiguous or t.is_contiguous()):
+        return
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}, the device of the first argument, got {t.device}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if contiguous and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _call(dev, fn, *args):
-    """fn(*args, stream) with ``dev`` current, on its current stream."""
-    cuda = _torch().cuda
-    if dev.index == cuda.current_device():
-        fn(*args, cuda.current_stream(dev).cuda_stream)
+def _call(dev, name, *args):
+    """The C entry point with ``dev`` current, on its current stream."""
+    torch = _torch()
+    fn = getattr(_lib.load(), name)
+    index = dev.index
+    if index == torch.cuda.current_device():
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
-        with cuda.device(dev):
-            fn(*args, cuda.current_stream(dev).cuda_stream)
+        with torch.cuda.device(dev):
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if rc != _lib.FA_OK:
+        raise _lib.FAError(name, rc)
 
 
 def _strides(name, t):
     """(batch, token) strides of [B, N, H, d] whose heads are contiguous."""
     B, N, H, d = t.shape
-    st = t.stride()
-    if (st[3] != 1 and d > 1) or (st[2] != d and H > 1):
+    sb, sn, sh, sd = t.stride()
+    if (sd != 1 and d > 1) or (sh != d and H > 1):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return (st[0] if B > 1 else 0), (st[1] if N > 1 else 0)
+    return (sb if B > 1 else 0), (sn if N > 1 else 0)
 
 
 # ---------------------------------------------------------------------------
@@ -114,29 +134,29 @@ def rotary_magnitude(factor: float) -> float:
 
 def _rotary(q, k, positions, table, interleaved, magnitude, inverse, q_out, k_out):
     torch = _torch()
-    dev = q.device
-    B, N, Hq, d = q.shape
-    dt = _dt(q)
-    _check("q", q, q.dtype, q.shape, dev, contiguous=False)
-    _check("table", table, torch.int64, table.shape[:1], dev)
-    _check("positions", positions, torch.int32, (N,) if positions.dim() == 1 else (B, N), dev)
+    dt, dev, dtype, shape = _dt(q), _device(q), q.dtype, q.shape
+    B, N, Hq, d = shape
+    each = positions.dim() == 2
+    _check("positions", positions, torch.int32, (B, N) if each else (N,), dev)
+    pairs = table.numel()
+    _check("table", table, torch.int64, (pairs,), dev)
     q_st, k_st, Hkv, kp, kop = _strides("q", q), (0, 0), 0, 0, 0
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        q_out = q.new_empty(shape)
     else:
-        _check("q_out", q_out, q.dtype, q.shape, dev)
+        _check("q_out", q_out, dtype, shape, dev)
     if k is not None:
         Hkv = k.shape[2]
-        _check("k", k, q.dtype, (B, N, Hkv, d), dev, contiguous=False)
+        shape = (B, N, Hkv, d)
+        _check("k", k, dtype, shape, dev, contiguous=False)
         k_st = _strides("k", k)
         if k_out is None:
-            k_out = torch.empty(k.shape, dtype=q.dtype, device=dev)
+            k_out = k.new_empty(shape)
         else:
-            _check("k_out", k_out, q.dtype, k.shape, dev)
+            _check("k_out", k_out, dtype, shape, dev)
         kp, kop = k.data_ptr(), k_out.data_ptr()
-    _call(dev, _lib.fa_rotary, q.data_ptr(), kp, q_out.data_ptr(), kop, positions.data_ptr(), table.data_ptr(), B, N,
-          Hq, Hkv, d, 2 * table.numel(), interleaved, inverse, magnitude, *q_st, *k_st,
-          N if positions.dim() == 2 else 0, dt)
+    _call(dev, "fa_rotary", q.data_ptr(), kp, q_out.data_ptr(), kop, positions.data_ptr(), table.data_ptr(), B, N,
+          Hq, Hkv, d, 2 * pairs, int(interleaved), int(inverse), magnitude, *q_st, *k_st, N if each else 0, dt)
     return q_out, k_out
 
 
@@ -163,10 +183,12 @@ def rotary_bwd(dq, dk, positions, table, interleaved: bool = False, magnitude: f
 def _check_cache(k8, v8, k_scale, v_scale, B, Hkv, d, dev):
     torch = _torch()
     Nk_max = k8.shape[1]
-    _check("k8", k8, torch.uint8, (B, Nk_max, Hkv, d), dev)
-    _check("v8", v8, torch.uint8, (B, Nk_max, Hkv, d), dev)
-    _check("k_scale", k_scale, torch.float32, (B, Hkv, Nk_max), dev)
-    _check("v_scale", v_scale, torch.float32, (B, Hkv, Nk_max), dev)
+    shape = (B, Nk_max, Hkv, d)
+    _check("k8", k8, torch.uint8, shape, dev)
+    _check("v8", v8, torch.uint8, shape, dev)
+    shape = (B, Hkv, Nk_max)
+    _check("k_scale", k_scale, torch.float32, shape, dev)
+    _check("v_scale", v_scale, torch.float32, shape, dev)
     return Nk_max
 
 
@@ -177,16 +199,14 @@ def fp8_cache_append(k, v, k8, v8, k_scale, v_scale, start, counts=None):
     cache are dropped.  k and v may be slices of one packed projection (heads contiguous).
     """
     torch = _torch()
-    dev = k.device
+    dt, dev = _dt(k), _device(k)
     B, n, Hkv, d = k.shape
-    dt = _dt(k)
-    _check("k", k, k.dtype, k.shape, dev, contiguous=False)
     _check("v", v, k.dtype, k.shape, dev, contiguous=False)
     Nk_max = _check_cache(k8, v8, k_scale, v_scale, B, Hkv, d, dev)
     _check("start", start, torch.int32, (B,), dev)
     if counts is not None:
         _check("counts", counts, torch.int32, (B,), dev)
-    _call(dev, _lib.fa_fp8_cache_append, k.data_ptr(), v.data_ptr(), k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(),
+    _call(dev, "fa_fp8_cache_append", k.data_ptr(), v.data_ptr(), k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(),
           v_scale.data_ptr(), start.data_ptr(), 0 if counts is None else counts.data_ptr(), B, n, Hkv, Nk_max, d,
           *_strides("k", k), *_strides("v", v), dt)
 
@@ -195,14 +215,14 @@ def fp8_cache_read(k8, v8, k_scale, v_scale, seqlens_k, Nk: int | None = None, d
     """The first Nk rows (None: all) of an E4M3 cache as (k, v) [B, Nk, Hkv, d] in ``dtype`` (bf16 by
     default), rows past seqlens_k[b] zero, via ``fa_fp8_cache_read``."""
     torch = _torch()
-    dev = k8.device
+    dev = _device(k8)
     B, Nk_max, Hkv, d = k8.shape
     _check_cache(k8, v8, k_scale, v_scale, B, Hkv, d, dev)
     _check("seqlens_k", seqlens_k, torch.int32, (B,), dev)
     Nk = Nk_max if Nk is None else Nk
-    k = torch.empty(B, Nk, Hkv, d, dtype=torch.bfloat16 if dtype is None else dtype, device=dev)
+    k = k8.new_empty((B, Nk, Hkv, d), dtype=torch.bfloat16 if dtype is None else dtype)
     v = torch.empty_like(k)
-    _call(dev, _lib.fa_fp8_cache_read, k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+    _call(dev, "fa_fp8_cache_read", k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
           seqlens_k.data_ptr(), k.data_ptr(), v.data_ptr(), B, Nk, Hkv, Nk_max, d, _dt(k))
     return k, v
 
@@ -210,24 +230,35 @@ def fp8_cache_read(k8, v8, k_scale, v_scale, seqlens_k, Nk: int | None = None, d
 # ---------------------------------------------------------------------------
 # decode
 # ---------------------------------------------------------------------------
-def _decode_buffers(q, seqlens_k, splits, workspace, out, lse):
+@functools.lru_cache(maxsize=1024)
+def _plan(device, B, Hq, Hkv, Np, Nk_max, d, prefix_splits, num_splits):
+    """Split counts (None: the library's suggestion) and workspace bytes: functions of the sizes alone."""
+    with _torch().cuda.device(device):
+        if prefix_splits is None:
+            prefix_splits = _lib.fa_decode_prefix_splits(B, Hq, Hkv, Np) if Np else 0
+        if num_splits is None:
+            num_splits = _lib.fa_decode_fp8_num_splits(B, Hkv, Nk_max)
+    return prefix_splits, num_splits, _lib.fa_decode_workspace_bytes(B, Hq, prefix_splits + num_splits, d)
+
+
+def _decode_buffers(q, seqlens_k, need, workspace, out, lse):
     torch = _torch()
-    dev = q.device
-    B, Nq, Hq, d = q.shape
-    _check("q", q, q.dtype, (B, 1, Hq, d), dev)
+    dev, dtype = q.device, q.dtype
+    B, _, Hq, d = q.shape
+    shape = (B, 1, Hq, d)
+    _check("q", q, dtype, shape, dev)
     _check("seqlens_k", seqlens_k, torch.int32, (B,), dev)
-    need = _lib.fa_decode_workspace_bytes(B, Hq, splits, d)
     if workspace is None:
-        workspace = torch.empty(need, device=dev, dtype=torch.uint8)
+        workspace = q.new_empty(need, dtype=torch.uint8)
     elif workspace.device != dev or not workspace.is_contiguous() or \
             workspace.numel() * workspace.element_size() < need:
         raise ValueError(f"workspace must be contiguous, on the device of q and hold {need} bytes")
     if out is None:
-        out = torch.empty(B, 1, Hq, d, device=dev, dtype=q.dtype)
+        out = q.new_empty(shape)
     else:
-        _check("out", out, q.dtype, (B, 1, Hq, d), dev)
+        _check("out", out, dtype, shape, dev)
     if lse is None:
-        lse = torch.empty(B, Hq, 1, device=dev, dtype=torch.float32)
+        lse = q.new_empty((B, Hq, 1), dtype=torch.float32)
     else:
         _check("lse", lse, torch.float32, (B, Hq, 1), dev)
     return workspace, out, lse
@@ -236,16 +267,14 @@ def _decode_buffers(q, seqlens_k, splits, workspace, out, lse):
 def decode_fp8(q, k8, v8, k_scale, v_scale, seqlens_k, num_splits: int | None = None, scale: float | None = None,
                workspace=None, out=None, lse=None):
     """One-token attention over an E4M3 cache; returns O [B, 1, Hq, d] and LSE [B, Hq, 1] (``fa_decode_fp8``)."""
-    dev = q.device
+    dt, dev = _dt(q), _device(q)
     B, _, Hq, d = q.shape
     Hkv = k8.shape[2]
-    dt = _dt(q)
     Nk_max = _check_cache(k8, v8, k_scale, v_scale, B, Hkv, d, dev)
     scale = 1.0 / math.sqrt(d) if scale is None else scale
-    if num_splits is None:
-        num_splits = _lib.fa_decode_fp8_num_splits(B, Hkv, Nk_max)
-    workspace, out, lse = _decode_buffers(q, seqlens_k, num_splits, workspace, out, lse)
-    _call(dev, _lib.fa_decode_fp8, q.data_ptr(), k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+    _, num_splits, need = _plan(dev.index, B, Hq, Hkv, 0, Nk_max, d, None, num_splits)
+    workspace, out, lse = _decode_buffers(q, seqlens_k, need, workspace, out, lse)
+    _call(dev, "fa_decode_fp8", q.data_ptr(), k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
           seqlens_k.data_ptr(), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), B, Hq, Hkv, Nk_max, d, scale,
           num_splits, dt)
     return out, lse
@@ -261,12 +290,12 @@ def decode_shared_prefix(q, k_prefix, v_prefix, k_cache, v_cache, seqlens_k, k_s
     codes with ``k_scale`` and ``v_scale`` (``fa_decode_shared_prefix``).
     """
     torch = _torch()
-    dev = q.device
+    dt, dev, dtype = _dt(q), _device(q), q.dtype
     B, _, Hq, d = q.shape
-    Np, Hkv = k_prefix.shape[1:3]
-    dt = _dt(q)
-    _check("k_prefix", k_prefix, q.dtype, (1, Np, Hkv, d), dev)
-    _check("v_prefix", v_prefix, q.dtype, (1, Np, Hkv, d), dev)
+    _, Np, Hkv, _ = k_prefix.shape
+    shape = (1, Np, Hkv, d)
+    _check("k_prefix", k_prefix, dtype, shape, dev)
+    _check("v_prefix", v_prefix, dtype, shape, dev)
     if k_cache.dtype == torch.uint8:
         if k_scale is None or v_scale is None:
             raise ValueError("an E4M3 cache comes with k_scale and v_scale")
@@ -276,16 +305,14 @@ def decode_shared_prefix(q, k_prefix, v_prefix, k_cache, v_cache, seqlens_k, k_s
         if k_scale is not None or v_scale is not None:
             raise ValueError("k_scale and v_scale go with uint8 E4M3 caches")
         Nk_max = k_cache.shape[1]
-        _check("k_cache", k_cache, q.dtype, (B, Nk_max, Hkv, d), dev)
-        _check("v_cache", v_cache, q.dtype, (B, Nk_max, Hkv, d), dev)
+        shape = (B, Nk_max, Hkv, d)
+        _check("k_cache", k_cache, dtype, shape, dev)
+        _check("v_cache", v_cache, dtype, shape, dev)
         ksp = vsp = 0
     scale = 1.0 / math.sqrt(d) if scale is None else scale
-    if prefix_splits is None:
-        prefix_splits = _lib.fa_decode_prefix_splits(B, Hq, Hkv, Np)
-    if num_splits is None:
-        num_splits = _lib.fa_decode_fp8_num_splits(B, Hkv, Nk_max)
-    workspace, out, lse = _decode_buffers(q, seqlens_k, prefix_splits + num_splits, workspace, out, lse)
-    _call(dev, _lib.fa_decode_shared_prefix, q.data_ptr(), k_prefix.data_ptr(), v_prefix.data_ptr(),
+    prefix_splits, num_splits, need = _plan(dev.index, B, Hq, Hkv, Np, Nk_max, d, prefix_splits, num_splits)
+    workspace, out, lse = _decode_buffers(q, seqlens_k, need, workspace, out, lse)
+    _call(dev, "fa_decode_shared_prefix", q.data_ptr(), k_prefix.data_ptr(), v_prefix.data_ptr(),
           k_cache.data_ptr(), v_cache.data_ptr(), ksp, vsp, seqlens_k.data_ptr(), out.data_ptr(), lse.data_ptr(),
           workspace.data_ptr(), B, Hq, Hkv, Np, Nk_max, d, scale, prefix_splits, num_splits, dt)
     return out, lse

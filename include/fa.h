@@ -397,7 +397,7 @@ fa_status fa_rotary(const void* q, const void* k, void* q_out, void* k_out, cons
  *   counts: DEVICE int32 [B] or NULL, how many of the n rows a sequence appends
  *     (NULL: all n; values outside [0, n] are clamped into that range).
  * Rows whose place lies outside [0, Nk_max) are dropped, and every other row of
- * the cache is left as it was.
+ * the cache is left as it was.  B * n * Hkv < 2^31.
  */
 fa_status fa_fp8_cache_append(const void* k, const void* v, void* k8, void* v8, float* k_scale, float* v_scale,
                               const int* start, const int* counts, int B, int n, int Hkv, int Nk_max, int d,
@@ -407,7 +407,7 @@ fa_status fa_fp8_cache_append(const void* k, const void* v, void* k8, void* v8, 
 /*
  * The first Nk (<= Nk_max) rows of such a cache as 16-bit values (code times
  * scale, rounded once): k, v [B,Nk,Hkv,d], as fa_fwd takes them.  Rows at or
- * past seqlens_k[b] (DEVICE int32 [B]) are written as zeros.
+ * past seqlens_k[b] (DEVICE int32 [B]) are written as zeros.  B * Nk * Hkv < 2^31.
  */
 fa_status fa_fp8_cache_read(const void* k8, const void* v8, const float* k_scale, const float* v_scale,
                             const int* seqlens_k, void* k, void* v, int B, int Nk, int Hkv, int Nk_max, int d,
