@@ -44,6 +44,7 @@
 #include <type_traits>
 
 #include "common.cuh"
+#include "kernels.h"
 #include "serving.h"
 
 namespace fa {
@@ -53,12 +54,15 @@ constexpr int kThreads = 128;
 constexpr float kStale = 6.f;  // log2 units that a score may exceed the reference m by
 constexpr int kMinUnit = -112;  // smallest e of the weights' unit (all powers of two below stay normal)
 
-// Shape of a warp's ring: kStep keys a block, kStages blocks.
+// Shape of a warp's ring: kStep keys a block, kStages blocks.  Two of 32 keys leave room for three CTAs
+// on an SM (99 KB in flight); three of 32 were 2 % slower on 32768-key sequences and up to 30 % on
+// short ones, three of 16 as fast there and 8 % slower here.  Persistent CTAs that load the next
+// item's first block under the merge gained 3 % on 500-key sequences and cost 13 % on ragged long ones.
 template <int D, bool F8>
 struct Ring {
   static constexpr int kRow = D * (F8 ? 1 : 2);          // bytes of a K or V row
   static constexpr int kStep = kRow <= 128 ? 32 : 16;    // keys per block
-  static constexpr int kStages = 3;
+  static constexpr int kStages = 2;
   static constexpr int kTile = kStep * kRow;
   static constexpr int kStage = 2 * kTile + (F8 ? 2 * kStep * 4 : 0);  // K, V, their scales
   static constexpr int kWarp = kStages * kStage;
@@ -443,69 +447,75 @@ __global__ void __launch_bounds__(kThreads) cache_decode_kernel(CacheDecodeArgs 
   if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-// Merge: one CTA per (h_q, b).  Every warp first takes all live splits' LSE (one lane each, 32 at a
-// time) to the shared maximum, then sums its quarter of the splits, whose loads do not depend on one
-// another.
-template <typename T, int D>
+// Merge: WARPS warps per (h_q, b), each over its share of the live splits.  Every warp first takes
+// all splits' LSE (a lane each, 32 at a time) to the shared maximum; the sums' loads then do not
+// depend on one another.
+template <typename T, int D, int WARPS>
 __global__ void __launch_bounds__(kThreads) cache_combine_kernel(CacheDecodeArgs p) {
   __shared__ float red[4][D];
   __shared__ float red_l[4];
-  const int h = blockIdx.x, b = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kCols = D / 32;  // columns per lane
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = warp % WARPS;
+  const long row = (long)blockIdx.x * (4 / WARPS) + warp / WARPS;  // b Hq + h
+  const long nrows = (long)p.B * p.Hq;
   const int S = p.prefix_splits + p.num_splits;
-  int n = p.seqlens[b];
+  int n = 0;
+  if (row < nrows) n = p.seqlens[row / p.Hq];
   n = n < 0 ? 0 : (n > p.Nk_max ? p.Nk_max : n);
-  const int live = p.prefix_splits + (n + p.chunk - 1) / p.chunk;
-  const long base = ((long)b * p.Hq + h) * S;
-  const bool ok = FA_IN_BOUNDS(p.status, base + S - 1, (long)p.B * p.Hq * S);
+  int live = p.prefix_splits + (n + p.chunk - 1) / p.chunk;
+  const long base = row * S;
+  if (!(row < nrows && FA_IN_BOUNDS(p.status, base + S - 1, nrows * S))) live = 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   float mx = -INFINITY;
-  for (int s = lane; ok && s < live; s += 32) mx = fmaxf(mx, p.lse_part[base + s]);
+  for (int s = lane; s < live; s += 32) mx = fmaxf(mx, p.lse_part[base + s]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
   const float mu = mx == -INFINITY ? 0.f : mx;
   float l = 0.f;
-  float o[D / 32];
+  float o[kCols];
 #pragma unroll
-  for (int i = 0; i < D / 32; ++i) o[i] = 0.f;
-  if (ok) {
-#pragma unroll 4
-    for (int s = warp; s < live; s += 4) {
-      const float w = ex2((p.lse_part[base + s] - mu) * kLog2e);
-      const float* row = p.o_part + (base + s) * D + lane * (D / 32);
-      float x[D / 32];
-      if constexpr (D == 128) {
-        const float4 f = *reinterpret_cast<const float4*>(row);
-        x[0] = f.x;
-        x[1] = f.y;
-        x[2] = f.z;
-        x[3] = f.w;
-      } else {
-        const float2 f = *reinterpret_cast<const float2*>(row);
-        x[0] = f.x;
-        x[1] = f.y;
-      }
-      l += w;
+  for (int i = 0; i < kCols; ++i) o[i] = 0.f;
+#pragma unroll 8
+  for (int s = part; s < live; s += WARPS) {
+    const float w = ex2((p.lse_part[base + s] - mu) * kLog2e);
+    const float* src = p.o_part + (base + s) * D + lane * kCols;
+    float x[kCols];
+    if constexpr (D == 128) {
+      const float4 f = *reinterpret_cast<const float4*>(src);
+      x[0] = f.x;
+      x[1] = f.y;
+      x[2] = f.z;
+      x[3] = f.w;
+    } else {
+      const float2 f = *reinterpret_cast<const float2*>(src);
+      x[0] = f.x;
+      x[1] = f.y;
+    }
+    l += w;
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) o[i] += w * x[i];
+    for (int i = 0; i < kCols; ++i) o[i] += w * x[i];
+  }
+  if constexpr (WARPS == 4) {
+#pragma unroll
+    for (int i = 0; i < kCols; ++i) red[warp][lane * kCols + i] = o[i];
+    if (lane == 0) red_l[warp] = l;
+    __syncthreads();
+    if (warp > 0) return;
+    l = (red_l[0] + red_l[1]) + (red_l[2] + red_l[3]);
+#pragma unroll
+    for (int i = 0; i < kCols; ++i) {
+      const int col = lane * kCols + i;
+      o[i] = (red[0][col] + red[1][col]) + (red[2][col] + red[3][col]);
     }
   }
+  if (row >= nrows) return;
+  const float inv = 1.f / l;
 #pragma unroll
-  for (int i = 0; i < D / 32; ++i) red[warp][lane * (D / 32) + i] = o[i];
-  if (lane == 0) red_l[warp] = l;
-  __syncthreads();
-  const int col = threadIdx.x;
-  if (col >= D) return;
-  const float lt = (red_l[0] + red_l[1]) + (red_l[2] + red_l[3]);
-  const float ot = (red[0][col] + red[1][col]) + (red[2][col] + red[3][col]);
-  const long row = (long)b * p.Hq + h;
-  const float out = lt == 0.f ? 0.f : ot / lt;  // no key: O = 0, LSE = -inf
-  uint16_t* go = static_cast<uint16_t*>(p.o) + row * D;
-  T v;
-  if constexpr (Elem<T>::kBf16) v = __float2bfloat16_rn(out); else v = __float2half_rn(out);
-  if (FA_IN_BOUNDS(p.status, row, (long)p.B * p.Hq)) {
-    go[col] = *reinterpret_cast<uint16_t*>(&v);
-    if (col == 0) p.lse[row] = mu + logf(lt);
-  }
+  for (int i = 0; i < kCols; ++i) o[i] = l == 0.f ? 0.f : o[i] * inv;  // no key: O = 0, LSE = -inf
+  uint32_t* go = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o) + row * D + lane * kCols);
+#pragma unroll
+  for (int i = 0; i < kCols / 2; ++i) go[i] = Elem<T>::pack(o[2 * i], o[2 * i + 1]);
+  if (lane == 0) p.lse[row] = mu + logf(l);
 }
 
 template <typename T, int D, bool F8, int NB>
@@ -538,8 +548,13 @@ cudaError_t launch_part_d(const CacheDecodeArgs& a, int after_prefix, cudaStream
 
 template <typename T, int D>
 cudaError_t launch_combine(const CacheDecodeArgs& a, cudaStream_t s) {
+  const long rows = (long)a.B * a.Hq;
+  // four warps a row for many splits or few rows
+  const bool four = a.prefix_splits + a.num_splits > 8 || rows < 4l * device_sm_count();
+  const long blocks = four ? rows : (rows + 3) / 4;
+  if (blocks > 0x7fffffffL) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(a.Hq, a.B);
+  cfg.gridDim = dim3((unsigned)blocks);
   cfg.blockDim = dim3(kThreads);
   cfg.stream = s;
   cudaLaunchAttribute attr{};
@@ -547,7 +562,7 @@ cudaError_t launch_combine(const CacheDecodeArgs& a, cudaStream_t s) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, cache_combine_kernel<T, D>, a);
+  return cudaLaunchKernelEx(&cfg, four ? cache_combine_kernel<T, D, 4> : cache_combine_kernel<T, D, 1>, a);
 }
 
 }  // namespace

@@ -20,6 +20,13 @@
 //    heads x (128 / G) sequences of q [B, Hq, d], so row r is head r % G of
 //    sequence r / G.  Rows past G (128 / G), up to 127, hold whatever the
 //    shared memory held; a row's results never reach another row's;
+//  * with one query tile, a K/V tile is taken in two halves of 64 keys with an S
+//    buffer each (S_h, P_h over its first columns): while a row's exponentials of
+//    one half run, the tensor core multiplies the other half's P and refills its S
+//    (1.57 us a K/V tile; 1.75 us with one S buffer of 128 keys, whose softmax and
+//    products take turns).  Two query tiles overlap each other that way, and the
+//    shorter products of halves only cost them (1.95 us a K/V tile; 2.4 us in
+//    halves);
 //  * the output is fp32, staged 32 columns at a time and written by a TMA box of
 //    the same shape into o_part [B, Hq, S, d].
 #include <cuda.h>
@@ -47,6 +54,39 @@ constexpr int kRegsSoftmax = 200;
 constexpr int kRegsControl = 104;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: rescale O when m grows by more than 2^8
 
+// 2^x for two values on the FMA and integer pipes, as exp2_fma2 (sm100.cuh) does it but by a
+// degree-5 minimax polynomial (gen_exp2_poly.py 5; relative error 2.4e-7 against the 7.5e-5 of degree
+// 3): a prefix may hold a single key, whose LSE is log2 of one such value and is kept to fp32 here.
+__device__ __forceinline__ float2 exp2_fma2_fine(float2 x) {
+  x.x = fmaxf(x.x, -126.f);
+  x.y = fmaxf(x.y, -126.f);
+  const float2 t = __fadd2_rn(x, make_float2(12582912.f, 12582912.f));
+  const float2 n = __fadd2_rn(t, make_float2(-12582912.f, -12582912.f));
+  const float2 f = __ffma2_rn(n, make_float2(-1.f, -1.f), x);
+  float2 q = make_float2(1.327647245e-03f, 1.327647245e-03f);
+  q = __ffma2_rn(q, f, make_float2(9.675540961e-03f, 9.675540961e-03f));
+  q = __ffma2_rn(q, f, make_float2(5.550713092e-02f, 5.550713092e-02f));
+  q = __ffma2_rn(q, f, make_float2(2.402212024e-01f, 2.402212024e-01f));
+  q = __ffma2_rn(q, f, make_float2(6.931469440e-01f, 6.931469440e-01f));
+  q = __ffma2_rn(q, f, make_float2(1.000000119e+00f, 1.000000119e+00f));
+  return make_float2(__int_as_float(__float_as_int(q.x) + (__float_as_int(t.x) << 23)),
+                     __int_as_float(__float_as_int(q.y) + (__float_as_int(t.y) << 23)));
+}
+// max(a, b, c), NaN if one of them is.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// Of every eight column pairs of a score block, how many take it instead of ex2.approx (measured at
+// 0, 2, 3 and 4: one query tile is fastest at 2 by 0.3 us in 34, two at 0 by 2.5 %).
+template <int NT>
+__device__ __forceinline__ float2 exp2_pair(float2 x, int pair) {
+  constexpr int K = NT == 1 ? 2 : 0;
+  if (((pair + 1) * K) / 8 != (pair * K) / 8) return exp2_fma2_fine(x);
+  return make_float2(ex2(x.x), ex2(x.y));
+}
+
 template <int D, int NT>
 struct Smem {
   static constexpr int kPanel = 128 * 128;  // one [128 rows][128 bytes] swizzled panel
@@ -56,13 +96,17 @@ struct Smem {
   static constexpr int kOffV = kOffK + kStages * kTile;
   static constexpr int kOffStage = kOffV + kStages * kTile;  // 32 fp32 columns per query tile
   static constexpr int kOffBar = kOffStage + NT * kPanel;
-  enum { kBarQ = 0, kBarKFull = 1, kBarKEmpty = 3, kBarVFull = 5, kBarVEmpty = 7, kBarS = 9, kBarP = 11, kBarO = 13,
-         kBarDrain = 15, kBarQEmpty = 16, kBarOFree = 17, kBarStageFull = 19, kBarStageDone = 21, kNumBars = 23 };
+  enum { kBarQ = 0, kBarKFull = 1, kBarKEmpty = 3, kBarVFull = 5, kBarVEmpty = 7, kBarS = 9, kBarP = 13, kBarDrain = 17,
+         kBarQEmpty = 18, kBarOFree = 19, kBarStageFull = 21, kBarStageDone = 23, kNumBars = 25 };
+  // kBarS / kBarP + 2 t + h: S (P) of half h of query tile t is there.  S completes once more per work
+  // than there are tiles: the last time when the last PV of that half has finished.
   static constexpr int kOffTmem = kOffBar + kNumBars * 8;
   static constexpr int kOffAbort = kOffTmem + 4;
   static constexpr int kBytes = kOffAbort + 4 + 1024;  // + slack to align the base to 1024 B
   static_assert(kBytes <= 232448, "shared memory per CTA exceeded");
   static constexpr int kThreads = 128 * (NT + 1);
+  static constexpr int kHalves = NT == 1 ? 2 : 1;  // S buffers of a query tile
+  static constexpr int kWidth = kBN / kHalves;     // their keys
   // TMEM columns: S_t, then O_t
   static constexpr uint32_t col_s(int t) { return 128u * t; }
   static constexpr uint32_t col_o(int t) { return 128u * NT + 128u * t; }
@@ -112,10 +156,7 @@ __global__ void __launch_bounds__(Smem<D, NT>::kThreads, 1)
 
   if (tid == 0) {
     for (int i = 0; i < L::kNumBars; ++i)
-      mbar_init(bar(i), (i == L::kBarP || i == L::kBarP + 1 || i == L::kBarOFree || i == L::kBarOFree + 1 ||
-                         i == L::kBarStageFull || i == L::kBarStageFull + 1)
-                            ? kBM
-                            : 1);
+      mbar_init(bar(i), (i >= L::kBarP && i < L::kBarP + 4) || (i >= L::kBarOFree && i < L::kBarStageDone) ? kBM : 1);
     *abort_flag = 0;
     fence_mbar_init();
     fence_proxy_async_smem();
@@ -197,40 +238,46 @@ __global__ void __launch_bounds__(Smem<D, NT>::kThreads, 1)
     // ------------------------------------------------------------------ MMA issuer
     if (lane == 0) {
       constexpr bool kBf16 = Elem<T>::kBf16;
-      constexpr uint32_t idq = idesc_f16(kBf16, kBM, kBN, false);
+      constexpr uint32_t idq = idesc_f16(kBf16, kBM, L::kWidth, false);
       constexpr uint32_t idv = idesc_f16(kBf16, kBM, D, true);
-      auto qk = [&](int t, int st) {
+      auto qk = [&](int t, int h, int st) {  // scores of keys kWidth h .. of the tile
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t ko = (kk >> 2) * L::kPanel + (kk & 3) * 32;
           const uint64_t a = sdesc_sw128(sb + L::kOffQ + t * L::kTile + ko, 16, 1024);
-          const uint64_t bd = sdesc_sw128(sb + L::kOffK + st * L::kTile + ko, 16, 1024);
-          mma_ss(tbase + L::col_s(t), a, bd, idq, kk > 0 ? 1u : 0u);
+          const uint64_t bd = sdesc_sw128(sb + L::kOffK + st * L::kTile + ko + h * (L::kWidth * 128), 16, 1024);
+          mma_ss(tbase + L::col_s(t) + L::kWidth * h, a, bd, idq, kk > 0 ? 1u : 0u);
         }
       };
-      auto pv = [&](int t, int st, bool first) {
+      auto pv = [&](int t, int h, int st, bool first) {
 #pragma unroll
-        for (int kk = 0; kk < kBN / 16; ++kk) {
+        for (int kk = 0; kk < L::kWidth / 16; ++kk) {
           // V stored [keys][d]: B is N(=d)-major; 16 keys = two 8-row groups of 128 B
-          const uint64_t bd = sdesc_sw128(sb + L::kOffV + st * L::kTile + kk * 2048, L::kPanel, 1024);
-          mma_ts(tbase + L::col_o(t), tbase + L::col_s(t) + kk * 8, bd, idv, (!first || kk > 0) ? 1u : 0u);
+          const uint64_t bd =
+              sdesc_sw128(sb + L::kOffV + st * L::kTile + (h * (L::kWidth / 16) + kk) * 2048, L::kPanel, 1024);
+          mma_ts(tbase + L::col_o(t), tbase + L::col_s(t) + L::kWidth * h + kk * 8, bd, idv, (!first || kk > 0) ? 1u : 0u);
         }
       };
       bool ok = true;
-      int g = 0;  // K/V tiles consumed so far by this CTA; S/P barriers complete once per tile
+      int g = 0;  // K/V tiles consumed so far by this CTA; P barriers complete once per tile
       int wl = 0;
       for (int w = blockIdx.x; ok && w < p.num_work; w += gridDim.x, ++wl) {
         const int nblk = blocks_of(work_at(p, w));
         ok = mbar_wait(bar(L::kBarQ), wl & 1, abort_flag, p.status) &&
              mbar_wait(bar(L::kBarKFull + (g & 1)), (g >> 1) & 1, abort_flag, p.status);
+        // the previous epilogue has read O_t: only then may S complete again (its waiters tell two
+        // neighbouring completions apart, not three) and O_t be overwritten
+        for (int t = 0; ok && t < NT && wl > 0; ++t)
+          ok = mbar_wait(bar(L::kBarOFree + t), (wl - 1) & 1, abort_flag, p.status);
         if (!ok) break;
         tc_fence_after();
-        // the previous work's last PV ran before these in issue order; its S/P buffers are free
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          qk(t, g & 1);
-          mma_commit(bar(L::kBarS + t));
-        }
+        for (int h = 0; h < L::kHalves; ++h)
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            qk(t, h, g & 1);
+            mma_commit(bar(L::kBarS + 2 * t + h));
+          }
         mma_commit(bar(L::kBarKEmpty + (g & 1)));
         if (nblk == 1) mma_commit(bar(L::kBarQEmpty));
         for (int j = 0; ok && j < nblk; ++j, ++g) {
@@ -239,24 +286,23 @@ __global__ void __launch_bounds__(Smem<D, NT>::kThreads, 1)
           const int st1 = (g + 1) & 1, u1 = (g + 1) >> 1;
           ok = mbar_wait(bar(L::kBarVFull + st), u & 1, abort_flag, p.status);
 #pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            ok = ok && mbar_wait(bar(L::kBarP + t), g & 1, abort_flag, p.status);
-            // the first PV of a work overwrites O_t: the previous epilogue must have read it
-            if (ok && j == 0 && wl > 0) ok = mbar_wait(bar(L::kBarOFree + t), (wl - 1) & 1, abort_flag, p.status);
-            if (!ok) break;
-            tc_fence_after();
-            pv(t, st, j == 0);
-            if (!more) mma_commit(bar(L::kBarO + t));
-            if (more) {
-              if (t == 0) {
-                ok = mbar_wait(bar(L::kBarKFull + st1), u1 & 1, abort_flag, p.status);
-                if (!ok) break;
+          for (int h = 0; h < L::kHalves; ++h)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+              ok = ok && mbar_wait(bar(L::kBarP + 2 * t + h), g & 1, abort_flag, p.status);
+              if (ok) {
                 tc_fence_after();
+                pv(t, h, st, j == 0 && h == 0);
+                if (more && h == 0 && t == 0) ok = mbar_wait(bar(L::kBarKFull + st1), u1 & 1, abort_flag, p.status);
               }
-              qk(t, st1);  // overwrites S_t / P_t after PV in issue order
-              mma_commit(bar(L::kBarS + t));
+              if (ok) {
+                if (more) {
+                  tc_fence_after();
+                  qk(t, h, st1);  // overwrites S_h / P_h of the tile after its PV, in issue order
+                }
+                mma_commit(bar(L::kBarS + 2 * t + h));
+              }
             }
-          }
           if (!ok) break;
           if (!more) mma_commit(bar(L::kBarVEmpty + st));  // inside a work the softmax warps free V (below)
           if (more && j + 2 == nblk) mma_commit(bar(L::kBarQEmpty));  // last score MMAs issued
@@ -278,98 +324,107 @@ __global__ void __launch_bounds__(Smem<D, NT>::kThreads, 1)
     const uint32_t tO = tbase + lane_off + L::col_o(t);
     const float c = p.scale_log2;
     bool ok = true;
-    int g = 0;  // K/V tiles processed so far by this CTA
+    int g = 0;  // K/V tiles processed so far by this CTA; S has completed g + wl times
     int wl = 0;
     for (int w = blockIdx.x; ok && w < p.num_work; w += gridDim.x, ++wl) {
       const Work x = work_at(p, w);
       const int nblk = blocks_of(x), key0 = x.s * p.chunk;
       float m_ref = -INFINITY, l = 0.f;
       for (int j = 0; j < nblk; ++j, ++g) {
-        ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarS + t), g & 1, abort_flag, p.status));
-        if (!ok) break;
-        if (t == NT - 1 && wq == 0 && lane == 0 && j != 0) {
-          // the last tile's S of tile g is complete, and with it every MMA issued before it: the
-          // score MMAs of tile g (its K stage is free) and the PV of tile g - 1 (its V stage is)
-          mbar_arrive(bar(L::kBarKEmpty + (g & 1)));
-          mbar_arrive(bar(L::kBarVEmpty + ((g - 1) & 1)));
-        }
-        tc_fence_after();
-        float s[kBN];
-        {
-          uint32_t r0[32], r1[32], r2[32], r3[32];
-          tmem_ld32(tS + 0, r0);
-          tmem_ld32(tS + 32, r1);
-          tmem_ld32(tS + 64, r2);
-          tmem_ld32(tS + 96, r3);
-          tmem_wait_ld();
-          reg_fence(r0);
-          reg_fence(r1);
-          reg_fence(r2);
-          reg_fence(r3);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            s[i] = __uint_as_float(r0[i]);
-            s[32 + i] = __uint_as_float(r1[i]);
-            s[64 + i] = __uint_as_float(r2[i]);
-            s[96 + i] = __uint_as_float(r3[i]);
+#pragma unroll 1
+        for (int h = 0; h < L::kHalves; ++h) {
+          ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarS + 2 * t + h), (g + wl) & 1, abort_flag, p.status));
+          if (!ok) break;
+          if (t == NT - 1 && h == L::kHalves - 1 && wq == 0 && lane == 0 && j != 0) {
+            // the last S of tile g is complete, and with it every MMA issued before it: the score
+            // MMAs of tile g (its K stage is free) and the PV of tile g - 1 (its V stage is)
+            mbar_arrive(bar(L::kBarKEmpty + (g & 1)));
+            mbar_arrive(bar(L::kBarVEmpty + ((g - 1) & 1)));
           }
-        }
-        const int lim = p.Np - (key0 + j * kBN);  // keys of this tile inside the prefix
-        if (lim < kBN) {
+          tc_fence_after();
+          const uint32_t tSh = tS + L::kWidth * h;
+          float s[L::kWidth];
+          {
+            uint32_t r[L::kWidth / 32][32];
 #pragma unroll
-          for (int i = 0; i < kBN; ++i)
-            if (i >= lim) s[i] = -INFINITY;
-        }
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int i = 0; i < kBN; i += 8) {
-          mx[0] = max3(mx[0], s[i], s[i + 1]);
-          mx[1] = max3(mx[1], s[i + 2], s[i + 3]);
-          mx[2] = max3(mx[2], s[i + 4], s[i + 5]);
-          mx[3] = max3(mx[3], s[i + 6], s[i + 7]);
-        }
-        const float mxs = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-        const bool resc = mxs > m_ref + kRescaleThreshold;
-        const float corr = resc ? ex2(m_ref - mxs) : 1.f;
-        if (resc) m_ref = mxs;
-        l *= corr;
-        const float mu = (m_ref == -INFINITY) ? 0.f : m_ref;
-        const float2 c2 = make_float2(c, c), nm2 = make_float2(-mu, -mu);
-        float2 rs0 = make_float2(0.f, 0.f), rs1 = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t pk[32];
-#pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            const int c0 = 64 * half + 2 * i;
-            const float2 xa = __ffma2_rn(make_float2(s[c0], s[c0 + 1]), c2, nm2);
-            const float2 xb = __ffma2_rn(make_float2(s[c0 + 2], s[c0 + 3]), c2, nm2);
-            const float2 a = make_float2(ex2(xa.x), ex2(xa.y)), bb = make_float2(ex2(xb.x), ex2(xb.y));
-            rs0 = __fadd2_rn(rs0, a);
-            rs1 = __fadd2_rn(rs1, bb);
-            pk[i] = Elem<T>::pack(a.x, a.y);
-            pk[i + 1] = Elem<T>::pack(bb.x, bb.y);
-          }
-          tmem_st32(tS + 32 * half, pk);
-        }
-        l += (rs0.x + rs0.y) + (rs1.x + rs1.y);
-        if (__any_sync(0xffffffffu, resc && j > 0)) {
-#pragma unroll
-          for (int q = 0; q < D / 32; ++q) {
-            uint32_t r[32];
-            tmem_ld32(tO + q * 32, r);
+            for (int q = 0; q < L::kWidth / 32; ++q) tmem_ld32(tSh + 32 * q, r[q]);
             tmem_wait_ld();
-            reg_fence(r);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * corr);
-            tmem_st32(tO + q * 32, r);
+            for (int q = 0; q < L::kWidth / 32; ++q) {
+              reg_fence(r[q]);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) s[32 * q + i] = __uint_as_float(r[q][i]);
+            }
           }
+          const int lim = p.Np - (key0 + j * kBN + L::kWidth * h);  // keys of this S inside the prefix
+          if (lim < L::kWidth) {
+#pragma unroll
+            for (int i = 0; i < L::kWidth; ++i)
+              if (i >= lim) s[i] = -INFINITY;
+          }
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int i = 0; i < L::kWidth; i += 8) {
+            mx[0] = max3_nan(mx[0], s[i], s[i + 1]);
+            mx[1] = max3_nan(mx[1], s[i + 2], s[i + 3]);
+            mx[2] = max3_nan(mx[2], s[i + 4], s[i + 5]);
+            mx[3] = max3_nan(mx[3], s[i + 6], s[i + 7]);
+          }
+          const float mxs = max3_nan(max3_nan(mx[0], mx[1], mx[2]), mx[3], mx[3]) * c;
+          const bool resc = mxs > m_ref + kRescaleThreshold;
+          const float corr = resc ? ex2(m_ref - mxs) : 1.f;
+          if (resc) m_ref = mxs;
+          l *= corr;
+          const float mu = (m_ref == -INFINITY) ? 0.f : m_ref;
+          const float2 c2 = make_float2(c, c), nm2 = make_float2(-mu, -mu);
+          float2 rs0 = make_float2(0.f, 0.f), rs1 = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int q = 0; q < L::kWidth / 32; ++q) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+              const int c0 = 32 * q + 2 * i;
+              const float2 xa = __ffma2_rn(make_float2(s[c0], s[c0 + 1]), c2, nm2);
+              const float2 xb = __ffma2_rn(make_float2(s[c0 + 2], s[c0 + 3]), c2, nm2);
+              const float2 a = exp2_pair<NT>(xa, 16 * q + i), bb = exp2_pair<NT>(xb, 16 * q + i + 1);
+              rs0 = __fadd2_rn(rs0, a);
+              rs1 = __fadd2_rn(rs1, bb);
+              pk[i] = Elem<T>::pack(a.x, a.y);
+              pk[i + 1] = Elem<T>::pack(bb.x, bb.y);
+            }
+            tmem_st16(tSh + 16 * q, pk);
+          }
+          l += (rs0.x + rs0.y) + (rs1.x + rs1.y);
+          // a NaN or +inf score makes the row NaN, also where the polynomial would clamp it away
+          if (!(mxs < INFINITY)) l = NAN;
+          if (__any_sync(0xffffffffu, resc && j + h > 0)) {
+            if constexpr (L::kHalves == 2) {
+              // the other half's last PV must have finished (with one S buffer this S is behind it)
+              ok = __all_sync(0xffffffffu,
+                              mbar_wait(bar(L::kBarS + 2 * t + (h ^ 1)), (g + wl + h) & 1, abort_flag, p.status));
+              if (!ok) break;
+              tc_fence_after();
+            }
+#pragma unroll
+            for (int q = 0; q < D / 32; ++q) {
+              uint32_t r[32];
+              tmem_ld32(tO + q * 32, r);
+              tmem_wait_ld();
+              reg_fence(r);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * corr);
+              tmem_st32(tO + q * 32, r);
+            }
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(bar(L::kBarP + 2 * t + h));
         }
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(bar(L::kBarP + t));
+        if (!ok) break;
       }
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarO + t), wl & 1, abort_flag, p.status));
+      // the last PV has finished (of both halves: the first's was committed before the second's)
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarS + 2 * t + L::kHalves - 1), (g + wl) & 1, abort_flag,
+                                                  p.status));
       if (!ok) break;
       uint32_t r[D];
       // O_t: TMEM -> registers, then hand the TMEM columns back to the MMA thread at once
@@ -383,7 +438,8 @@ __global__ void __launch_bounds__(Smem<D, NT>::kThreads, 1)
       mbar_arrive(bar(L::kBarOFree + t));
 
       const int b0 = (x.rb * NT + t) * p.seqs;  // first sequence of this query tile
-      const float inv = l == 0.f ? 0.f : 1.f / l;  // every score -inf: O = 0, LSE = -inf
+      if (m_ref == -INFINITY && l == l) l = 0.f;  // every score -inf (clamped exponentials aside): O = 0, LSE = -inf
+      const float inv = l == 0.f ? 0.f : 1.f / l;
       const int b = b0 + rr / p.G;
       if (rr < p.G * p.seqs && b < p.B) {
         const long li = ((long)b * p.Hq + x.hk * p.G + rr % p.G) * p.S + x.s;
@@ -460,7 +516,7 @@ cudaError_t launch(const CacheDecodeArgs& a, cudaStream_t s) {
   constexpr int smem = Smem<D, NT>::kBytes;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  const int grid = (int)std::min<long long>(work, device_sm_count());
+  const int grid = (int)std::min<long long>(work, a.prefix_ctas > 0 ? a.prefix_ctas : device_sm_count());
   kern<<<grid, Smem<D, NT>::kThreads, smem, s>>>(mq, mk, mv, mo, p);
   return cudaGetLastError();
 }

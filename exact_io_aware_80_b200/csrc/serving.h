@@ -81,6 +81,7 @@ struct CacheDecodeArgs {
   int B, Hq, Hkv, Np, Nk_max, d;
   int prefix_splits, prefix_chunk;  // keys per prefix split, a multiple of 128
   int num_splits, chunk;            // keys per cache split, a multiple of 64
+  int prefix_ctas = 0;              // CTAs of the prefix kernel (0: one per SM)
   float scale;
   int bf16;
   int* status;

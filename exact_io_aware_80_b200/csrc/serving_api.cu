@@ -168,9 +168,13 @@ fa_status fa_fp8_cache_read(const void* k8, const void* v8, const float* k_scale
 int fa_decode_fp8_num_splits(int B, int Hkv, int Nk_max, int num_sms) {
   if (B < 1 || Hkv < 1 || Nk_max < 1) return 1;
   const long long units = (long long)B * Hkv;
-  const long long want = std::max<long long>(1, (26ll * sm_count(num_sms) + units - 1) / units);
-  const int cap = (Nk_max + 255) / 256;
-  const int splits = (int)std::min<long long>(want, cap);
+  const int sms = sm_count(num_sms);
+  // A split's keys take about 6 ns each and every further split 0.12 us of merging: sqrt(Nk / 20)
+  // splits balance the two (one sequence, 8 KV heads, 32768 keys: 32 splits 18.9 us, 16 21.7, 128 27.4).
+  // Beyond 3.5 (b, h_kv, split) units per SM further splits only add merging (16 sequences of 2000
+  // keys: 4 splits 14.7 us, 8 18.4), but long ragged sequences take two (64 of 32768: 503 against 533 us).
+  const long long fill = std::max<long long>(units > 2 * sms && Nk_max >= 8192 ? 2 : 1, 7ll * sms / (2 * units));
+  int splits = (int)std::min<long long>(fill, std::max(1, (int)std::sqrt(Nk_max / 20.0)));
   const int chunk = fa_decode_chunk(Nk_max, splits);
   return (Nk_max + chunk - 1) / chunk;
 }

@@ -142,7 +142,7 @@ def _rotary(q, k, positions, table, interleaved, magnitude, inverse, q_out, k_ou
     _check("table", table, torch.int64, (pairs,), dev)
     q_st, k_st, Hkv, kp, kop = _strides("q", q), (0, 0), 0, 0, 0
     if q_out is None:
-        q_out = q.new_empty(shape)
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
     else:
         _check("q_out", q_out, dtype, shape, dev)
     if k is not None:
@@ -151,7 +151,7 @@ def _rotary(q, k, positions, table, interleaved, magnitude, inverse, q_out, k_ou
         _check("k", k, dtype, shape, dev, contiguous=False)
         k_st = _strides("k", k)
         if k_out is None:
-            k_out = k.new_empty(shape)
+            k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
         else:
             _check("k_out", k_out, dtype, shape, dev)
         kp, kop = k.data_ptr(), k_out.data_ptr()
@@ -254,7 +254,7 @@ def _decode_buffers(q, seqlens_k, need, workspace, out, lse):
             workspace.numel() * workspace.element_size() < need:
         raise ValueError(f"workspace must be contiguous, on the device of q and hold {need} bytes")
     if out is None:
-        out = q.new_empty(shape)
+        out = torch.empty_like(q)
     else:
         _check("out", out, dtype, shape, dev)
     if lse is None:

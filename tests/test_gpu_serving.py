@@ -372,6 +372,30 @@ def test_decode_shared_prefix(fa, B, Hq, Hkv, Np, Nk, d, dt, fp8, ps, cs):
                  max(F8_STEP, torch.finfo(DT[dt]).eps / 2), F8_FLOOR)
 
 
+@pytest.mark.parametrize("B", [2, 40])
+def test_decode_shared_prefix_passes_on_nan(fa, B):
+    """One bad key of the prefix, in every column of a tile's exponentials, makes its KV head's rows NaN
+    and no other's; so does a query row, for itself; so does a +inf score."""
+    Hq, Hkv, Np, Nk, d = 8, 2, 200, 4, 64
+    lens = [b % 5 for b in range(B)]
+    q, args, _, _ = prefix_case(fa, B, Hq, Hkv, Np, Nk, d, "bf16", False, lens, 65)
+    for key in list(range(0, 16)) + [127, 128, 199]:
+        kp = args[1].clone()
+        kp[0, key, 1, 3] = float("nan") if key % 2 else float("inf")
+        qq = args[0].clone()
+        qq[..., 3] = qq[..., 3].abs() + 0.5
+        o, lse = fa.decode_shared_prefix(qq, kp, *args[2:])
+        assert o[:, 0, 4:].isnan().all() and torch.isfinite(o[:, 0, :4]).all() and torch.isfinite(lse[:, :4]).all()
+    qq = args[0].clone()
+    qq[B - 1, 0, 2, 7] = float("nan")
+    o, lse = fa.decode_shared_prefix(qq, *args[1:])
+    bad = torch.zeros(B, Hq, dtype=torch.bool, device="cuda")
+    bad[B - 1, 2] = True
+    assert torch.equal(o[:, 0].isnan().all(-1), bad) and torch.equal(o[:, 0].isnan().any(-1), bad)
+    assert torch.equal(lse[:, :, 0].isnan(), bad)
+    done(fa)
+
+
 def test_decode_shared_prefix_with_more_work_than_sms(fa):
     """Work tiles beyond one per SM: 5 row blocks x 8 KV heads x 8 splits, so a CTA takes several."""
     B, Hq, Hkv, Np, Nk, d = 300, 32, 8, 1024, 4, 64
