@@ -19,7 +19,7 @@ from ._lib import (FAError, fa_bwd, fa_bwd_dkdv, fa_bwd_dq, fa_bwd_preprocess, f
                    fa_decode_workspace_bytes, fa_fp8_quantize_qk, fa_fp8_quantize_qkv, fa_fp8_quantize_v,
                    fa_fp8_v_workspace_bytes, fa_fwd,
                    fa_bwd_dropout, fa_fwd_blocksparse, fa_fwd_dropout, fa_fwd_fp8, fa_get_device_status, fa_version)
-from ._lib import (fa_decode_fp8, fa_decode_fp8_num_splits, fa_decode_prefix_splits, fa_decode_shared_prefix,  # noqa: F401
+from ._lib import (fa_decode_fp8, fa_decode_fp8_workspace_bytes, fa_decode_prefix_splits, fa_decode_shared_prefix,  # noqa: F401
                    fa_fp8_cache_append, fa_fp8_cache_read, fa_rotary)
 from .serving import (decode_fp8, decode_shared_prefix, fp8_cache_append, fp8_cache_read, rotary_bwd,  # noqa: F401
                       rotary_fwd, rotary_magnitude, rotary_table)
@@ -33,7 +33,7 @@ __all__ = [
     "fa_fp8_v_workspace_bytes", "fa_fwd_fp8", "attention_fwd_blocksparse", "fa_fwd_blocksparse",
     "attention_fwd_dropout", "attention_bwd_dropout", "fa_fwd_dropout", "fa_bwd_dropout", "FAError",
     "rotary_table", "rotary_magnitude", "rotary_fwd", "rotary_bwd", "fp8_cache_append", "fp8_cache_read", "decode_fp8",
-    "decode_shared_prefix", "fa_rotary", "fa_fp8_cache_append", "fa_fp8_cache_read", "fa_decode_fp8_num_splits",
+    "decode_shared_prefix", "fa_rotary", "fa_fp8_cache_append", "fa_fp8_cache_read", "fa_decode_fp8_workspace_bytes",
     "fa_decode_fp8", "fa_decode_prefix_splits", "fa_decode_shared_prefix",
 ]
 

@@ -61,10 +61,10 @@ SIGNATURES = {
     "fa_rotary": (_I, [_P] * 6 + [_I] * 8 + [_F] + [_L] * 5 + [_I, _P]),
     "fa_fp8_cache_append": (_I, [_P] * 8 + [_I] * 5 + [_L] * 4 + [_I, _P]),
     "fa_fp8_cache_read": (_I, [_P] * 7 + [_I] * 5 + [_I, _P]),
-    "fa_decode_fp8_num_splits": (_I, [_I, _I, _I, _I]),
-    "fa_decode_fp8": (_I, [_P] * 9 + [_I] * 5 + [_F, _I, _I, _P]),
-    "fa_decode_prefix_splits": (_I, [_I, _I, _I, _I, _I]),
-    "fa_decode_shared_prefix": (_I, [_P] * 11 + [_I] * 6 + [_F, _I, _I, _I, _P]),
+    "fa_decode_fp8_workspace_bytes": (ctypes.c_size_t, [_I] * 5),
+    "fa_decode_fp8": (_I, [_P] * 9 + [_I] * 5 + [_F, _I, _P]),
+    "fa_decode_prefix_splits": (_I, [_I] * 8),
+    "fa_decode_shared_prefix": (_I, [_P] * 11 + [_I] * 6 + [_F, _I, _I, _P]),
     "fa_get_device_status": (_I, [_P]),
     "fa_watchdog_selftest": (_I, [_I, _P]),
     "fa_status_string": (ctypes.c_char_p, [_I]),
@@ -244,26 +244,25 @@ def fa_fp8_cache_read(k8, v8, k_scale, v_scale, seqlens_k, k, v, B, Nk, Hkv, Nk_
                                                                 Nk_max, d, dt, stream))
 
 
-def fa_decode_fp8_num_splits(B, Hkv, Nk_max, num_sms=0):
-    return load().fa_decode_fp8_num_splits(B, Hkv, Nk_max, num_sms)
+def fa_decode_fp8_workspace_bytes(B, Hq, Hkv, prefix_splits, d):
+    return load().fa_decode_fp8_workspace_bytes(B, Hq, Hkv, prefix_splits, d)
 
 
-def fa_decode_fp8(q, k8, v8, k_scale, v_scale, seqlens_k, o, lse, workspace, B, Hq, Hkv, Nk_max, d, scale, num_splits,
-                  dt, stream):
+def fa_decode_fp8(q, k8, v8, k_scale, v_scale, seqlens_k, o, lse, workspace, B, Hq, Hkv, Nk_max, d, scale, dt, stream):
     return _check("fa_decode_fp8", load().fa_decode_fp8(q, k8, v8, k_scale, v_scale, seqlens_k, o, lse, workspace, B,
-                                                        Hq, Hkv, Nk_max, d, scale, num_splits, dt, stream))
+                                                        Hq, Hkv, Nk_max, d, scale, dt, stream))
 
 
-def fa_decode_prefix_splits(B, Hq, Hkv, Np, num_sms=0):
-    return load().fa_decode_prefix_splits(B, Hq, Hkv, Np, num_sms)
+def fa_decode_prefix_splits(B, Hq, Hkv, Np, Nk_max, d, fp8_cache, num_sms=0):
+    return load().fa_decode_prefix_splits(B, Hq, Hkv, Np, Nk_max, d, int(fp8_cache), num_sms)
 
 
 def fa_decode_shared_prefix(q, k_prefix, v_prefix, k_cache, v_cache, k_scale, v_scale, seqlens_k, o, lse, workspace,
-                            B, Hq, Hkv, Np, Nk_max, d, scale, prefix_splits, num_splits, dt, stream):
+                            B, Hq, Hkv, Np, Nk_max, d, scale, prefix_splits, dt, stream):
     return _check("fa_decode_shared_prefix",
                   load().fa_decode_shared_prefix(q, k_prefix, v_prefix, k_cache, v_cache, k_scale, v_scale, seqlens_k,
                                                  o, lse, workspace, B, Hq, Hkv, Np, Nk_max, d, scale, prefix_splits,
-                                                 num_splits, dt, stream))
+                                                 dt, stream))
 
 
 def fa_watchdog_selftest(limit_us, stream):

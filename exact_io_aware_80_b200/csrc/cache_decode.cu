@@ -9,12 +9,22 @@
 // in 16 bits).  The codes are never multiplied out: s^k_j joins the score and
 // s^v_j the weight, so a key costs its d + 4 bytes twice.
 //
-// Partial pass: one CTA per (split, KV head, sequence).  The group's Hq / Hkv
-// query rows share every byte the CTA reads.  Each of the four warps streams
-// its own blocks of kStep keys through its own cp.async ring (no block barrier
-// until the end) with its own running (m, l, O); the warps merge through shared
-// memory.  Bound by HBM reads of the cache as long as the arithmetic per key is
-// small, which shapes the rest:
+// Work.  The keys of the batch, in blocks of kBlock, sequence after sequence, are
+// one line of W blocks, W from the lengths on the device; of the C CTAs (C <= W) of
+// each KV head, CTA i takes the blocks from i W / C to (i + 1) W / C, whatever
+// sequences they belong to, and leaves one partial (O, LSE of the group's rows) per
+// sequence that it touches, in its head's slot b + i -- along the line either
+// summand grows, so no two partials share one.  Every CTA has the same keys to read
+// however ragged the batch, and the CTAs of the Hkv heads, neighbours in the grid,
+// read the same tokens' rows together (a line through the heads as well, whose CTAs
+// stand at different tokens, lost 13 % of the bandwidth).
+//
+// A CTA.  The group's Hq / Hkv query rows share every byte it reads.  Each of the
+// four warps streams its own kStep keys of a block through its own two cp.async
+// buffers (no block barrier until a sequence's end) with its own running (m, l, O);
+// the warps merge through shared memory while the next block arrives.  Bound by
+// HBM reads of the cache as long as the arithmetic per key is small, which shapes
+// the rest:
 //  * The products are taken transposed, S^T = K Q^T and O^T = V^T P^T, so that
 //    keys and columns of d fill the MMA's 16 rows and the group its 8 columns
 //    (two column blocks for groups of 9 to 16): half the MMAs, exponentials and
@@ -54,24 +64,22 @@ constexpr int kThreads = 128;
 constexpr float kStale = 6.f;  // log2 units that a score may exceed the reference m by
 constexpr int kMinUnit = -112;  // smallest e of the weights' unit (all powers of two below stay normal)
 
-// Shape of a warp's ring: kStep keys a block, kStages blocks.  Two of 32 keys leave room for three CTAs
-// on an SM (99 KB in flight); three of 32 were 2 % slower on 32768-key sequences and up to 30 % on
-// short ones, three of 16 as fast there and 8 % slower here.  Persistent CTAs that load the next
-// item's first block under the merge gained 3 % on 500-key sequences and cost 13 % on ragged long ones.
+// A warp's two buffers of kStep keys each.  Two of them (99 KB in flight on an SM of three CTAs) leave
+// room for a third CTA: three of 32 keys were 2 % slower on 32768-key sequences and up to 30 % on
+// short ones.
 template <int D, bool F8>
 struct Ring {
   static constexpr int kRow = D * (F8 ? 1 : 2);          // bytes of a K or V row
   static constexpr int kStep = kRow <= 128 ? 32 : 16;    // keys per block
-  static constexpr int kStages = 2;
   static constexpr int kTile = kStep * kRow;
   static constexpr int kStage = 2 * kTile + (F8 ? 2 * kStep * 4 : 0);  // K, V, their scales
-  static constexpr int kWarp = kStages * kStage;
   static constexpr int kBlocks = kStep / 16;
 };
 template <int D, bool F8, int NB>
 struct Smem {
-  static constexpr int kRed = (4 * 8 * NB * (D + 2)) * 4;
-  static constexpr int kBytes = 4 * Ring<D, F8>::kWarp > kRed ? 4 * Ring<D, F8>::kWarp : kRed;
+  static constexpr int kOffM = 4 * 2 * Ring<D, F8>::kStage;  // m, l [4][8 NB] fp32, then the offset of each warp's O
+  static constexpr int kBytes = kOffM + 4 * 8 * NB * 2 * 4 + 4 * 4;
+  static_assert(8 * NB * D * 4 <= Ring<D, F8>::kStage, "a warp's O is merged through its free buffer");
 };
 
 // Byte offset of 16-byte chunk `c` of row `r` in a tile of ROW-byte rows, chunks permuted so that
@@ -110,82 +118,159 @@ __device__ __forceinline__ float rows_sum(float x) {
   return x + __shfl_xor_sync(0xffffffffu, x, 16);
 }
 
+// A run of blocks of one sequence, as one warp sees it.
+struct Item {
+  int b;
+  int first, hi;     // this warp's keys: kStep from first + i kBlock on, below hi
+  int nblk;
+  int pos;           // place of the run's first block on the line
+  int blk, blks;     // that block within the sequence, and the sequence's blocks
+};
+
 template <typename T, int D, bool F8, int NB>
-__global__ void __launch_bounds__(kThreads) cache_decode_kernel(CacheDecodeArgs p) {
+__global__ void __launch_bounds__(kThreads, cache_ctas_per_sm(D, F8, NB == 2)) cache_decode_kernel(CacheDecodeArgs p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   using R = Ring<D, F8>;
+  using L = Smem<D, F8, NB>;
   using M = typename std::conditional<F8, __half, T>::type;  // MMA operand type
   constexpr int MB = R::kBlocks;
+  constexpr int kBlock = 4 * R::kStep;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int s = blockIdx.x, hk = blockIdx.y, b = blockIdx.z;
-  const int G = p.Hq / p.Hkv;
-  const int S = p.prefix_splits + p.num_splits;
-  int n = p.seqlens[b];
-  n = n < 0 ? 0 : (n > p.Nk_max ? p.Nk_max : n);
-  const int lo = s * p.chunk;
-  const int hi = min(lo + p.chunk, n);
+  const int G = p.Hq / p.Hkv, hk = blockIdx.x % p.Hkv, cta = blockIdx.x / p.Hkv;
   // the merge, launched next as a programmatic dependent, may become resident; it waits for this
   // grid's end before it reads a partial
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (hi > lo) {
-    const uint32_t ring = smem_u32(smem) + warp * R::kWarp;
-    const uint8_t* const ring_g = smem + warp * R::kWarp;
-    const long row_bytes = (long)p.Hkv * R::kRow;
-    const long base = ((long)b * p.Nk_max * p.Hkv + hk) * R::kRow;
-    const uint8_t* const gk = static_cast<const uint8_t*>(p.k) + base;
-    const uint8_t* const gv = static_cast<const uint8_t*>(p.v) + base;
-    const long sbase = ((long)b * p.Hkv + hk) * p.Nk_max;
-    // this warp's blocks: keys lo + (4 i + warp) kStep ..
-    const int first = lo + warp * R::kStep;
-    const int nblk = first < hi ? (hi - first + 4 * R::kStep - 1) / (4 * R::kStep) : 0;
 
-    constexpr int kC = R::kRow / 16, kRows = 32 / kC;  // chunks per row, rows per pass of the warp
-    const int lr = lane / kC, lc = lane % kC;
-    auto load = [&](int i) {
-      const uint32_t st = ring + (i % R::kStages) * R::kStage;
-      const int key0 = first + i * 4 * R::kStep;
-      if (key0 + R::kStep <= hi) {
-        const uint8_t* pk = gk + (long)(key0 + lr) * row_bytes + 16 * lc;
-        const uint8_t* pv = gv + (long)(key0 + lr) * row_bytes + 16 * lc;
+  const uint32_t ring = smem_u32(smem) + warp * 2 * R::kStage;
+  const uint8_t* const ring_g = smem + warp * 2 * R::kStage;
+  float* const red_m = reinterpret_cast<float*>(smem + L::kOffM);
+  float* const red_l = red_m + 4 * 8 * NB;
+  uint32_t* const red_at = reinterpret_cast<uint32_t*>(red_l + 4 * 8 * NB);
+  const long row_bytes = (long)p.Hkv * R::kRow;
+
+  // W, this CTA's part [begin, end) of the line, and the sequence that begin lies in.  Every warp for
+// itself: a lane sums the blocks of a stretch of sequences, and the one whose stretch holds begin walks it
+  auto length = [&](int b) { return min(max(p.seqlens[b], 0), p.Nk_max); };
+  auto blocks = [&](int n) { return (n + kBlock - 1) / kBlock; };
+  int begin, end, W, C;  // W < 2^31: a block of a head takes 4 KB at least
+  int cb = 0, cblk = 0, cn = 0, cpos;  // the cursor: block cblk of sequence cb, of cn keys, at place cpos
+  {
+    const int per = (p.B + 31) / 32;
+    const int b0 = min(lane * per, p.B), b1 = min(b0 + per, p.B);
+    int mine = 0;
+#pragma unroll 4
+    for (int b = b0; b < b1; ++b) mine += blocks(length(b));
+    int upto = mine;
 #pragma unroll
-        for (int j = 0; j < R::kStep / kRows; ++j) {
-          cp_async16(st + chunk_at<R::kRow>(lr + j * kRows, lc), pk, true);
-          cp_async16(st + R::kTile + chunk_at<R::kRow>(lr + j * kRows, lc), pv, true);
-          pk += kRows * row_bytes;
-          pv += kRows * row_bytes;
-        }
-      } else {  // the last block: rows past hi as zeros
-#pragma unroll 1
-        for (int j = 0; j < R::kStep / kRows; ++j) {
-          const int r = lr + j * kRows;
-          const bool ok = key0 + r < hi;
-          const long off = ok ? (long)(key0 + r) * row_bytes + 16 * lc : 0;
-          cp_async16(st + chunk_at<R::kRow>(r, lc), gk + off, ok);
-          cp_async16(st + R::kTile + chunk_at<R::kRow>(r, lc), gv + off, ok);
-        }
-      }
-      if constexpr (F8) {
-        const int r = lane % R::kStep;
-        const bool ok = key0 + r < hi;
-        cp_async4(st + 2 * R::kTile + 4 * r, p.k_scale + sbase + (ok ? key0 + r : 0), ok);
-        cp_async4(st + 2 * R::kTile + 4 * (R::kStep + r), p.v_scale + sbase + (ok ? key0 + r : 0), ok);
-      }
-    };
-#pragma unroll
-    for (int i = 0; i < R::kStages - 1; ++i) {
-      if (i < nblk) load(i);
-      cp_async_commit();
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += t;
     }
-
-    // q as B fragments: column n = lane / 4 of block nb is query row 8 nb + n.  16-bit: k index =
-    // d; E4M3: k pairs 2c and 2c + 8 of step j are d = 16 j + 4 c + {0, 1} and {2, 3}, c = lane & 3
-    const uint16_t* gq = static_cast<const uint16_t*>(p.q) + ((long)b * p.Hq + (long)hk * G) * D;
-    uint32_t qf[NB][D / 16][2];
-    float cq[NB][2];  // scale log2(e) of rows 8 nb + 2 c + {0, 1}, without q's power of two
+    W = __shfl_sync(0xffffffffu, upto, 31);
+    C = min(p.cache_ctas / p.Hkv, W);  // a CTA without a block would be a gap in its neighbours' spans
+    begin = cta < C ? (int)((long long)cta * W / C) : W;
+    end = cta < C ? (int)((long long)(cta + 1) * W / C) : W;
+    int at = upto - mine;  // place of sequence b0
+    const bool here = begin < end && at <= begin && begin < upto;
+    if (here) {
+      cb = b0;
+      cn = length(cb);
+      while (begin >= at + blocks(cn)) {
+        at += blocks(cn);
+        cn = length(++cb);
+      }
+      cblk = begin - at;
+    }
+    const int who = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+    cb = __shfl_sync(0xffffffffu, cb, who & 31);
+    cn = __shfl_sync(0xffffffffu, cn, who & 31);
+    cblk = __shfl_sync(0xffffffffu, cblk, who & 31);
+    cpos = begin;
+  }
+  // the line's next run within [cpos, end)
+  auto next = [&](Item& it) {
+    if (cpos >= end) return false;
+    while (cblk == blocks(cn)) {  // this sequence is done, or has no key
+      cn = length(++cb);
+      cblk = 0;
+    }
+    it.b = cb;
+    it.pos = cpos;
+    it.blk = cblk;
+    it.blks = blocks(cn);
+    const int take = min(it.blks - cblk, end - cpos);
+    it.first = cblk * kBlock + warp * R::kStep;
+    it.hi = min((cblk + take) * kBlock, cn);
+    it.nblk = it.first < it.hi ? (it.hi - it.first + kBlock - 1) / kBlock : 0;
+    cpos += take;
+    cblk += take;
+    return true;
+  };
+  constexpr int kC = R::kRow / 16, kRows = 32 / kC;  // chunks per row, rows per pass of the warp
+  const int lr = lane / kC, lc = lane % kC;
+  // the loads run one block ahead of the products: `src` is the next block that this warp loads
+  struct {
+    const uint8_t *k, *v;    // this lane's chunk of row lr
+    const float *ks, *vs;    // the scales of row lane % kStep
+    int keys;                // rows of the block that are inside, kStep or more if it is full
+    int left;                // blocks of its item still to load
+  } src;
+  src.left = 0;
+  const long kstride = (long)kBlock * row_bytes;
+  auto aim = [&](const Item& it) {
+    const long row = ((long)it.b * p.Nk_max + it.first + lr) * p.Hkv + hk;
+    src.k = static_cast<const uint8_t*>(p.k) + row * R::kRow + 16 * lc;
+    src.v = static_cast<const uint8_t*>(p.v) + row * R::kRow + 16 * lc;
+    if constexpr (F8) {
+      const long at = ((long)it.b * p.Hkv + hk) * p.Nk_max + it.first + lane % R::kStep;
+      src.ks = p.k_scale + at;
+      src.vs = p.v_scale + at;
+    }
+    src.keys = it.hi - it.first;
+    src.left = it.nblk;
+  };
+  auto load = [&](int stage) {
+    const uint32_t st = ring + stage * R::kStage;
+    if (src.keys >= R::kStep) {
+      const uint8_t *pk = src.k, *pv = src.v;
+#pragma unroll
+      for (int j = 0; j < R::kStep / kRows; ++j) {
+        cp_async16(st + chunk_at<R::kRow>(lr + j * kRows, lc), pk, true);
+        cp_async16(st + R::kTile + chunk_at<R::kRow>(lr + j * kRows, lc), pv, true);
+        pk += kRows * row_bytes;
+        pv += kRows * row_bytes;
+      }
+    } else {  // a sequence's last block: rows past its end as zeros
+#pragma unroll 1
+      for (int j = 0; j < R::kStep / kRows; ++j) {
+        const int r = lr + j * kRows;
+        const bool ok = r < src.keys;
+        const long off = ok ? j * kRows * row_bytes : 0;
+        cp_async16(st + chunk_at<R::kRow>(r, lc), ok ? src.k + off : static_cast<const uint8_t*>(p.k), ok);
+        cp_async16(st + R::kTile + chunk_at<R::kRow>(r, lc), ok ? src.v + off : static_cast<const uint8_t*>(p.v), ok);
+      }
+    }
+    if constexpr (F8) {
+      const int r = lane % R::kStep;
+      const bool ok = r < src.keys;
+      cp_async4(st + 2 * R::kTile + 4 * r, ok ? src.ks : p.k_scale, ok);
+      cp_async4(st + 2 * R::kTile + 4 * (R::kStep + r), ok ? src.vs : p.v_scale, ok);
+      src.ks += kBlock;
+      src.vs += kBlock;
+    }
+    src.k += kstride;
+    src.v += kstride;
+    src.keys -= kBlock;
+    --src.left;
+  };
+  // q as B fragments: column n = lane / 4 of block nb is query row 8 nb + n.  16-bit: k index =
+  // d; E4M3: k pairs 2c and 2c + 8 of step j are d = 16 j + 4 c + {0, 1} and {2, 3}, c = lane & 3
+  uint32_t qf[NB][D / 16][2];
+  auto load_q = [&](const Item& it) {
+    const uint16_t* gq = static_cast<const uint16_t*>(p.q) + ((long)it.b * p.Hq + (long)hk * G) * D;
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
       const int row = 8 * nb + (lane >> 2), c = lane & 3;
-      float mul = 1.f, unmul = 1.f;
 #pragma unroll
       for (int j = 0; j < D / 16; ++j) {
         qf[nb][j][0] = qf[nb][j][1] = 0u;
@@ -201,6 +286,26 @@ __global__ void __launch_bounds__(kThreads) cache_decode_kernel(CacheDecodeArgs 
           }
         }
       }
+    }
+  };
+
+  Item cur;
+  bool have = next(cur);
+  int c0 = 0;  // buffer of the current item's first block
+  if (have) {
+    aim(cur);
+    if (cur.nblk > 0) load(0);
+    cp_async_commit();
+    load_q(cur);
+  }
+  while (have) {
+    Item nxt;
+    const bool more = next(nxt);
+
+    float cq[NB][2];  // scale log2(e) of rows 8 nb + 2 c + {0, 1}, without q's power of two
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      float unmul = 1.f;
       if constexpr (F8 && Elem<T>::kBf16) {
         float amax = 0.f;
 #pragma unroll
@@ -213,7 +318,7 @@ __global__ void __launch_bounds__(kThreads) cache_decode_kernel(CacheDecodeArgs 
         amax = quad_max(amax);
         // exponent of amax, kept where both powers of two are normal numbers
         const int ex = min(max((int)(__float_as_uint(amax) >> 23) - 127, -100), 126);
-        mul = pow2(14 - ex);
+        const float mul = pow2(14 - ex);
         unmul = pow2(ex - 14);
 #pragma unroll
         for (int j = 0; j < D / 16; ++j)
@@ -225,7 +330,7 @@ __global__ void __launch_bounds__(kThreads) cache_decode_kernel(CacheDecodeArgs 
       }
 #pragma unroll
       for (int e = 0; e < 2; ++e)
-        cq[nb][e] = p.scale * kLog2e * __shfl_sync(0xffffffffu, unmul, (2 * c + e) * 4);
+        cq[nb][e] = p.scale * kLog2e * __shfl_sync(0xffffffffu, unmul, (2 * (lane & 3) + e) * 4);
     }
 
     // O^T: acc[nb][i] holds columns 16 i + .. of d (rows of the MMA) for query rows 2 c + {0, 1}
@@ -244,13 +349,16 @@ __global__ void __launch_bounds__(kThreads) cache_decode_kernel(CacheDecodeArgs 
     constexpr float kLift = !F8 && !Elem<T>::kBf16 ? 8.f : 0.f;  // fp16 weights of a 16-bit cache
     int ev = kMinUnit;  // E4M3: 2^ev exceeds every V scale of this warp's keys so far
 
-    for (int i = 0; i < nblk; ++i) {
-      cp_async_wait<R::kStages - 2>();
-      __syncwarp();  // block i is there, and every lane is done with block i - 1
-      if (i + R::kStages - 1 < nblk) load(i + R::kStages - 1);
+    for (int i = 0; i < max(cur.nblk, 1); ++i) {
+      cp_async_wait<0>();
+      __syncwarp();  // block i is there, and every lane is done with the block before it
+      const int stage = (c0 + i) & 1;
+      if (src.left == 0 && more) aim(nxt);
+      if (src.left > 0) load(cur.nblk == 0 ? stage : stage ^ 1);
       cp_async_commit();
-      const uint32_t st = ring + (i % R::kStages) * R::kStage;
-      const int key0 = first + i * 4 * R::kStep;
+      if (cur.nblk == 0) break;
+      const uint32_t st = ring + stage * R::kStage;
+      const int key0 = cur.first + i * kBlock;
 
       float sc[MB][NB][4];  // keys 16 mb + lane / 4 + {0, 8}, rows 8 nb + 2 c + {0, 1}
 #pragma unroll
@@ -302,12 +410,12 @@ __global__ void __launch_bounds__(kThreads) cache_decode_kernel(CacheDecodeArgs 
             sc[mb][nb][2 * e + 1] *= cq[nb][1] * ks;
           }
         }
-      if (key0 + R::kStep > hi) {
+      if (key0 + R::kStep > cur.hi) {
 #pragma unroll
         for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
           for (int e = 0; e < 2; ++e)
-            if (key0 + 16 * mb + 8 * e + (lane >> 2) >= hi) {
+            if (key0 + 16 * mb + 8 * e + (lane >> 2) >= cur.hi) {
 #pragma unroll
               for (int nb = 0; nb < NB; ++nb) sc[mb][nb][2 * e] = sc[mb][nb][2 * e + 1] = -INFINITY;
             }
@@ -391,83 +499,98 @@ __global__ void __launch_bounds__(kThreads) cache_decode_kernel(CacheDecodeArgs 
         }
       }
     }
-    cp_async_wait<0>();
-    __syncthreads();
+    c0 += cur.nblk;  // the next item's first block is in buffer c0 & 1 or on its way there
+    if (more) load_q(nxt);
 
-    // merge the four warps through shared memory: O [4][8 NB][D], m and l [4][8 NB], fp32
-    float* red_o = reinterpret_cast<float*>(smem);
-    float* red_m = red_o + 4 * 8 * NB * D;
-    float* red_l = red_m + 4 * 8 * NB;
+    // merge the four warps: each leaves O [8 NB][D] in its free buffer, m and l [4][8 NB], fp32
+    __syncwarp();
+    const uint32_t at = (warp * 2 + ((c0 & 1) ^ 1)) * R::kStage;
+    float* const own = reinterpret_cast<float*>(smem + at);
+    if (lane == 0) red_at[warp] = at;
     const float back = F8 ? pow2(ev - 8) : 1.f;
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int row = warp * 8 * NB + 8 * nb + 2 * (lane & 3) + e;
+        const int row = 8 * nb + 2 * (lane & 3) + e;
         const float ls = rows_sum(l[nb][e]);
         if (lane < 4) {
-          red_m[row] = m[nb][e];
-          red_l[row] = ls;
+          red_m[warp * 8 * NB + row] = m[nb][e];
+          red_l[warp * 8 * NB + row] = ls;
         }
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           // MMA rows lane / 4 and lane / 4 + 8
-          const int c0 = 16 * k + (F8 ? 2 * (lane >> 2) : (lane >> 2)), c1 = F8 ? c0 + 1 : c0 + 8;
-          red_o[row * D + c0] = acc[nb][k][e] * back;
-          red_o[row * D + c1] = acc[nb][k][2 + e] * back;
+          const int col0 = 16 * k + (F8 ? 2 * (lane >> 2) : (lane >> 2)), col1 = F8 ? col0 + 1 : col0 + 8;
+          own[row * D + col0] = acc[nb][k][e] * back;
+          own[row * D + col1] = acc[nb][k][2 + e] * back;
         }
       }
     __syncthreads();
-    const long nparts = (long)p.B * p.Hq * S;
-    const long part0 = ((long)b * p.Hq + (long)hk * G) * S + p.prefix_splits + s;
-    for (int idx = tid; idx < G * D; idx += kThreads) {
-      const int g = idx / D, col = idx % D;
+    const long slots = (long)p.Hkv * (p.B + gridDim.x / p.Hkv);
+    const long slot = (long)hk * (p.B + gridDim.x / p.Hkv) + cur.b + cta;
+    // whoever has a sequence's first block knows which CTAs have the others
+    if (tid == 0 && cur.blk == 0 && hk == 0 && FA_IN_BOUNDS(p.status, cur.b, p.B))
+      p.spans[cur.b] = make_int2(cta, (int)(((long long)(cur.pos + cur.blks) * C - 1) / W));
+    for (int idx = 4 * tid; idx < G * D; idx += 4 * kThreads) {
+      const int g = idx / D;
       float mx = -INFINITY;
 #pragma unroll
       for (int w = 0; w < 4; ++w) mx = fmaxf(mx, red_m[w * 8 * NB + g]);
       const float mu = mx == -INFINITY ? 0.f : mx;  // every score -inf (l = 0) or NaN (l NaN)
-      float lt = 0.f, o = 0.f;
+      float lt = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
         // a warp with no finite score has l and O of 0 or NaN in any unit
         const float f = red_m[w * 8 * NB + g] == -INFINITY ? 1.f : ex2(red_m[w * 8 * NB + g] - mu);
+        const float4 x = *reinterpret_cast<const float4*>(smem + red_at[w] + 4 * idx);
         lt += red_l[w * 8 * NB + g] * f;
-        o += red_o[(w * 8 * NB + g) * D + col] * f;
+        o.x += x.x * f;
+        o.y += x.y * f;
+        o.z += x.z * f;
+        o.w += x.w * f;
       }
-      const long oi = part0 + (long)g * S;
-      if (FA_IN_BOUNDS(p.status, oi, nparts)) {
-        p.o_part[oi * D + col] = lt == 0.f ? 0.f : o / lt;
-        if (col == 0) p.lse_part[oi] = (mu - (mx == -INFINITY ? 0.f : kLift) + log2f(lt)) * kLn2;
+      if (FA_IN_BOUNDS(p.status, slot, slots)) {
+        const float inv = lt == 0.f ? 0.f : 1.f / lt;
+        *reinterpret_cast<float4*>(p.o_cache + slot * G * D + idx) =
+            lt == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+        if (idx % D == 0) p.lse_cache[slot * G + g] = (mu - (mx == -INFINITY ? 0.f : kLift) + log2f(lt)) * kLn2;
       }
     }
+    __syncthreads();  // the free buffers may be loaded into again
+    cur = nxt;
+    have = more;
   }
+  cp_async_wait<0>();
   // launched as a programmatic dependent of the prefix kernel: this grid must not end before that
   // one has, since the merge waits only for this one (without the launch attribute the wait
   // returns at once)
-  if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (blockIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-// Merge: WARPS warps per (h_q, b), each over its share of the live splits.  Every warp first takes
-// all splits' LSE (a lane each, 32 at a time) to the shared maximum; the sums' loads then do not
-// depend on one another.
+// Merge: WARPS warps per (h_q, b), each over its share of the row's partials: the prefix's splits, then
+// the cache's slots.  Every warp first takes all their LSE (a lane each, 32 at a time) to the shared
+// maximum; the sums' loads then do not depend on one another.
+constexpr int combine_threads(int warps) { return warps > 4 ? 32 * warps : 128; }
 template <typename T, int D, int WARPS>
-__global__ void __launch_bounds__(kThreads) cache_combine_kernel(CacheDecodeArgs p) {
-  __shared__ float red[4][D];
-  __shared__ float red_l[4];
+__global__ void __launch_bounds__(combine_threads(WARPS)) cache_combine_kernel(CacheDecodeArgs p) {
+  __shared__ float red[WARPS][D];
+  __shared__ float red_l[WARPS];
   constexpr int kCols = D / 32;  // columns per lane
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = warp % WARPS;
-  const long row = (long)blockIdx.x * (4 / WARPS) + warp / WARPS;  // b Hq + h
+  const long row = (long)blockIdx.x * (combine_threads(WARPS) / 32 / WARPS) + warp / WARPS;  // b Hq + h
   const long nrows = (long)p.B * p.Hq;
-  const int S = p.prefix_splits + p.num_splits;
-  int n = 0;
-  if (row < nrows) n = p.seqlens[row / p.Hq];
-  n = n < 0 ? 0 : (n > p.Nk_max ? p.Nk_max : n);
-  int live = p.prefix_splits + (n + p.chunk - 1) / p.chunk;
-  const long base = row * S;
-  if (!(row < nrows && FA_IN_BOUNDS(p.status, base + S - 1, nrows * S))) live = 0;
+  const int Sp = p.prefix_splits, G = p.Hq / p.Hkv;
+  const int b = (int)(row / p.Hq), h = (int)(row - (long)b * p.Hq), hk = h / G;
+  const bool has = row < nrows && p.seqlens[row < nrows ? b : 0] > 0 && p.Nk_max > 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int2 span = has ? p.spans[b] : make_int2(0, -1);
+  const int live = row < nrows ? Sp + span.y - span.x + 1 : 0;
+  const long slot0 = ((long)hk * (p.B + p.cache_ctas / p.Hkv) + b + span.x) * G + (h - hk * G);  // then G apart
+  auto lse_of = [&](int s) { return s < Sp ? p.lse_part[row * Sp + s] : p.lse_cache[slot0 + (long)(s - Sp) * G]; };
   float mx = -INFINITY;
-  for (int s = lane; s < live; s += 32) mx = fmaxf(mx, p.lse_part[base + s]);
+  for (int s = lane; s < live; s += 32) mx = fmaxf(mx, lse_of(s));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
   const float mu = mx == -INFINITY ? 0.f : mx;
@@ -477,8 +600,9 @@ __global__ void __launch_bounds__(kThreads) cache_combine_kernel(CacheDecodeArgs
   for (int i = 0; i < kCols; ++i) o[i] = 0.f;
 #pragma unroll 8
   for (int s = part; s < live; s += WARPS) {
-    const float w = ex2((p.lse_part[base + s] - mu) * kLog2e);
-    const float* src = p.o_part + (base + s) * D + lane * kCols;
+    const float w = ex2((lse_of(s) - mu) * kLog2e);
+    const float* src =
+        (s < Sp ? p.o_part + (row * Sp + s) * D : p.o_cache + (slot0 + (long)(s - Sp) * G) * D) + lane * kCols;
     float x[kCols];
     if constexpr (D == 128) {
       const float4 f = *reinterpret_cast<const float4*>(src);
@@ -495,17 +619,20 @@ __global__ void __launch_bounds__(kThreads) cache_combine_kernel(CacheDecodeArgs
 #pragma unroll
     for (int i = 0; i < kCols; ++i) o[i] += w * x[i];
   }
-  if constexpr (WARPS == 4) {
+  if constexpr (WARPS > 1) {
 #pragma unroll
     for (int i = 0; i < kCols; ++i) red[warp][lane * kCols + i] = o[i];
     if (lane == 0) red_l[warp] = l;
     __syncthreads();
     if (warp > 0) return;
-    l = (red_l[0] + red_l[1]) + (red_l[2] + red_l[3]);
+    l = 0.f;
 #pragma unroll
-    for (int i = 0; i < kCols; ++i) {
-      const int col = lane * kCols + i;
-      o[i] = (red[0][col] + red[1][col]) + (red[2][col] + red[3][col]);
+    for (int i = 0; i < kCols; ++i) o[i] = 0.f;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      l += red_l[w];
+#pragma unroll
+      for (int i = 0; i < kCols; ++i) o[i] += red[w][lane * kCols + i];
     }
   }
   if (row >= nrows) return;
@@ -525,7 +652,7 @@ cudaError_t launch_part(const CacheDecodeArgs& a, int after_prefix, cudaStream_t
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(a.num_splits, a.Hkv, a.B);
+  cfg.gridDim = dim3(a.cache_ctas);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
@@ -549,20 +676,26 @@ cudaError_t launch_part_d(const CacheDecodeArgs& a, int after_prefix, cudaStream
 template <typename T, int D>
 cudaError_t launch_combine(const CacheDecodeArgs& a, cudaStream_t s) {
   const long rows = (long)a.B * a.Hq;
-  // four warps a row for many splits or few rows
-  const bool four = a.prefix_splits + a.num_splits > 8 || rows < 4l * device_sm_count();
-  const long blocks = four ? rows : (rows + 3) / 4;
-  if (blocks > 0x7fffffffL) return cudaErrorInvalidValue;
+  // the more warps a row the more partials it may have, and the fewer rows there are to fill the SMs
+  const long parts = a.prefix_splits + a.cache_ctas / ((long)a.B * a.Hkv);
+  const int warps = parts > 16 && rows <= 4l * device_sm_count() ? 16 : parts > 8 || rows < 4l * device_sm_count() ? 4 : 1;
+  const int per = combine_threads(warps) / 32 / warps;  // rows a CTA
+  const long ctas = (rows + per - 1) / per;
+  if (ctas > 0x7fffffffL) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)blocks);
-  cfg.blockDim = dim3(kThreads);
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3(combine_threads(warps));
   cfg.stream = s;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, four ? cache_combine_kernel<T, D, 4> : cache_combine_kernel<T, D, 1>, a);
+  return cudaLaunchKernelEx(&cfg,
+                            warps == 16 ? cache_combine_kernel<T, D, 16>
+                            : warps == 4 ? cache_combine_kernel<T, D, 4>
+                                         : cache_combine_kernel<T, D, 1>,
+                            a);
 }
 
 }  // namespace

@@ -116,10 +116,9 @@ struct Smem {
 struct Params {
   float* lse_part;  // [B,Hq,S]
   int B, Hq, Hkv, Np, G, seqs;  // seqs = 128 / G sequences per query tile
-  int S;                        // splits per row of the partials (prefix and cache)
-  int splits, chunk;            // prefix splits and their keys
+  int S, chunk;                 // splits and their keys
   int row_blocks;               // NT query tiles each
-  int num_work;                 // splits * Hkv * row_blocks
+  int num_work;                 // S * Hkv * row_blocks
   float scale_log2;
   int* status;
 };
@@ -489,7 +488,7 @@ __global__ void __launch_bounds__(Smem<D, NT>::kThreads, 1)
 
 template <typename T, int D, int NT>
 cudaError_t launch(const CacheDecodeArgs& a, cudaStream_t s) {
-  const int G = a.Hq / a.Hkv, seqs = kBM / G, S = a.prefix_splits + a.num_splits;
+  const int G = a.Hq / a.Hkv, seqs = kBM / G, S = a.prefix_splits;
   const int type = Elem<T>::kBf16 ? kMapBf16 : kMapF16;
   CUtensorMap mq, mk, mv, mo;
   {
@@ -510,13 +509,13 @@ cudaError_t launch(const CacheDecodeArgs& a, cudaStream_t s) {
   const int rows = (a.B + NT * seqs - 1) / (NT * seqs);
   const long long work = (long long)rows * a.Hkv * a.prefix_splits;
   if (work > (1ll << 30)) return cudaErrorInvalidValue;
-  Params p{a.lse_part, a.B, a.Hq, a.Hkv, a.Np, G, seqs, S, a.prefix_splits, a.prefix_chunk, rows, (int)work,
+  Params p{a.lse_part, a.B, a.Hq, a.Hkv, a.Np, G, seqs, S, a.prefix_chunk, rows, (int)work,
            a.scale * kLog2e, a.status};
   auto kern = prefix_sm100_kernel<T, D, NT>;
   constexpr int smem = Smem<D, NT>::kBytes;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  const int grid = (int)std::min<long long>(work, a.prefix_ctas > 0 ? a.prefix_ctas : device_sm_count());
+  const int grid = (int)std::min<long long>(work, device_sm_count());
   kern<<<grid, Smem<D, NT>::kThreads, smem, s>>>(mq, mk, mv, mo, p);
   return cudaGetLastError();
 }

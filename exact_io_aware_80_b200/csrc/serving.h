@@ -66,22 +66,29 @@ cudaError_t launch_fp8_cache_append(const Fp8CacheArgs& a, cudaStream_t s);
 cudaError_t launch_fp8_cache_read(const Fp8CacheArgs& a, cudaStream_t s);
 
 // One-token attention over a cache (cache_decode.cu) and over a prefix that the whole batch
-// shares (prefix_sm100.cu), both writing normalised partials that one kernel merges:
-// o_part [B,Hq,S,d] and lse_part [B,Hq,S] fp32, S = prefix_splits + num_splits, the prefix's
-// splits first.  A sequence's splits past its length are neither written nor read.
+// shares (prefix_sm100.cu), both writing normalised fp32 partials that one kernel merges.  The
+// prefix's: o_part [B,Hq,Sp,d], lse_part [B,Hq,Sp], Sp = prefix_splits.  The caches': one per CTA
+// and sequence it reads keys of, o_cache [Hkv,slots,G,d], lse_cache [Hkv,slots,G] in slot
+// b + CTA, slots = B + cache_ctas / Hkv, with the first and last CTA of every sequence that has
+// keys in spans [B].
+// CTAs of the cache kernel that an SM holds: 67 KB of shared memory each and up to 168 registers a
+// thread, or 35 KB and 96 (128 for groups of 9 to 16 heads) with E4M3 rows of 64 values, which need
+// more of them in flight.
+constexpr int cache_ctas_per_sm(int d, bool fp8, bool wide) { return d == 64 && fp8 ? (wide ? 4 : 5) : 3; }
+constexpr int kMaxCacheCtas = 1024;
 struct CacheDecodeArgs {
   const void* q;  // [B,1,Hq,d]
   const void *kp, *vp;  // prefix [Np,Hkv,d] (prefix_splits > 0)
   const void *k, *v;    // cache [B,Nk_max,Hkv,d]: 16-bit, or E4M3 codes with scales [B,Hkv,Nk_max]
   const float *k_scale, *v_scale;
   const int* seqlens;
-  float *o_part, *lse_part;
+  float *o_part, *lse_part, *o_cache, *lse_cache;
+  int2* spans;
   void* o;
   float* lse;
   int B, Hq, Hkv, Np, Nk_max, d;
   int prefix_splits, prefix_chunk;  // keys per prefix split, a multiple of 128
-  int num_splits, chunk;            // keys per cache split, a multiple of 64
-  int prefix_ctas = 0;              // CTAs of the prefix kernel (0: one per SM)
+  int cache_ctas;                   // a multiple of Hkv, at most max(kMaxCacheCtas, Hkv)
   float scale;
   int bf16;
   int* status;

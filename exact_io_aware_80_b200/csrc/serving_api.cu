@@ -38,17 +38,55 @@ bool strides_aligned(long long bs, long long ts) { return bs % 8 == 0 && ts % 8 
 
 int sm_count(int num_sms) { return num_sms > 0 ? num_sms : fa::device_sm_count(); }
 
-fa_status check_decode(int B, int Hq, int Hkv, int Nk_max, int d, float scale, int num_splits, fa_dtype dt) {
-  if (B < 1 || Hq < 1 || Hkv < 1 || Nk_max < 1 || num_splits < 1) return FA_ERR_INVALID;
+fa_status check_decode(int B, int Hq, int Hkv, int Nk_max, int d, float scale, fa_dtype dt) {
+  if (B < 1 || Hq < 1 || Hkv < 1 || Nk_max < 1) return FA_ERR_INVALID;
   if (Hq % Hkv != 0) return FA_ERR_INVALID;
   if (!(scale >= 0.f) || std::isinf(scale)) return FA_ERR_INVALID;
   if (dt != FA_FP16 && dt != FA_BF16) return FA_ERR_UNSUPPORTED;
   if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
   if (Hq / Hkv > 16) return FA_ERR_UNSUPPORTED;  // one CTA holds a GQA group of at most 16 query heads
-  if (B > 65535 || Hkv > 65535 || Hq > 65535 || num_splits > 65535) return FA_ERR_UNSUPPORTED;
-  if (Nk_max > (1 << 30)) return FA_ERR_UNSUPPORTED;
-  if (num_splits > (Nk_max + 63) / 64) return FA_ERR_INVALID;
+  if (B > 65535 || Hkv > 65535 || Hq > 65535 || Nk_max > (1 << 30)) return FA_ERR_UNSUPPORTED;
   return FA_OK;
+}
+
+// Bytes of the partials, and where each kind lies: O of the prefix and of the caches, then the LSEs, then the spans.
+struct Workspace {
+  size_t o_cache, lse_part, lse_cache, spans, bytes;
+};
+Workspace workspace_of(int B, int Hq, int Hkv, int prefix_splits, int d) {
+  const size_t rows = (size_t)B * Hq * prefix_splits;
+  const size_t slots = ((size_t)B * Hkv + std::max(fa::kMaxCacheCtas, Hkv)) * (Hq / Hkv);
+  Workspace w;
+  w.o_cache = rows * d * 4;
+  w.lse_part = w.o_cache + slots * d * 4;
+  w.lse_cache = w.lse_part + rows * 4;
+  w.spans = (w.lse_cache + slots * 4 + 15) / 16 * 16;
+  w.bytes = w.spans + ((size_t)B * 8 + 255) / 256 * 256;
+  return w;
+}
+
+void place(fa::CacheDecodeArgs& a, void* workspace, const Workspace& w) {
+  unsigned char* base = static_cast<unsigned char*>(workspace);
+  a.o_part = reinterpret_cast<float*>(base);
+  a.o_cache = reinterpret_cast<float*>(base + w.o_cache);
+  a.lse_part = reinterpret_cast<float*>(base + w.lse_part);
+  a.lse_cache = reinterpret_cast<float*>(base + w.lse_cache);
+  a.spans = reinterpret_cast<int2*>(base + w.spans);
+}
+
+// CTAs of the cache kernel: the SMs that a prefix running beside it leaves (all of them once they are
+// few), two blocks of keys a CTA at least.
+int cache_ctas_of(int B, int Hkv, int Nk_max, int d, int G, bool fp8, int sms, long long prefix_ctas) {
+  const long long left = sms - prefix_ctas >= sms / 4 ? sms - prefix_ctas : sms;
+  const long long blocks = (long long)B * ((Nk_max + 127) / 128);
+  const long long most = std::min<long long>(fa::cache_ctas_per_sm(d, fp8, G > 8) * left, fa::kMaxCacheCtas) / Hkv;  // per KV head
+  return (int)(Hkv * std::max<long long>(1, std::min(most, blocks / 2)));
+}
+
+// Row blocks of the prefix kernel: 128 / G sequences to a query tile, one or two tiles to a block.
+long long prefix_row_blocks(int B, int G) {
+  const int seqs = 128 / G;
+  return B <= seqs ? 1 : (B + 2 * seqs - 1) / (2 * seqs);
 }
 
 }  // namespace
@@ -165,25 +203,16 @@ fa_status fa_fp8_cache_read(const void* k8, const void* v8, const float* k_scale
   return from_cuda(fa::launch_fp8_cache_read(a, static_cast<cudaStream_t>(stream)));
 }
 
-int fa_decode_fp8_num_splits(int B, int Hkv, int Nk_max, int num_sms) {
-  if (B < 1 || Hkv < 1 || Nk_max < 1) return 1;
-  const long long units = (long long)B * Hkv;
-  const int sms = sm_count(num_sms);
-  // A split's keys take about 6 ns each and every further split 0.12 us of merging: sqrt(Nk / 20)
-  // splits balance the two (one sequence, 8 KV heads, 32768 keys: 32 splits 18.9 us, 16 21.7, 128 27.4).
-  // Beyond 3.5 (b, h_kv, split) units per SM further splits only add merging (16 sequences of 2000
-  // keys: 4 splits 14.7 us, 8 18.4), but long ragged sequences take two (64 of 32768: 503 against 533 us).
-  const long long fill = std::max<long long>(units > 2 * sms && Nk_max >= 8192 ? 2 : 1, 7ll * sms / (2 * units));
-  int splits = (int)std::min<long long>(fill, std::max(1, (int)std::sqrt(Nk_max / 20.0)));
-  const int chunk = fa_decode_chunk(Nk_max, splits);
-  return (Nk_max + chunk - 1) / chunk;
+size_t fa_decode_fp8_workspace_bytes(int B, int Hq, int Hkv, int prefix_splits, int d) {
+  if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || prefix_splits < 0 || d < 1) return 0;
+  return workspace_of(B, Hq, Hkv, prefix_splits, d).bytes;
 }
 
 fa_status fa_decode_fp8(const void* q, const void* k8, const void* v8, const float* k_scale, const float* v_scale,
                         const int* seqlens_k, void* o, float* lse, void* workspace, int B, int Hq, int Hkv, int Nk_max,
-                        int d, float scale, int num_splits, fa_dtype dt, fa_stream_t stream) {
+                        int d, float scale, fa_dtype dt, fa_stream_t stream) {
   if (!q || !k8 || !v8 || !k_scale || !v_scale || !seqlens_k || !o || !lse || !workspace) return FA_ERR_INVALID;
-  const fa_status st = check_decode(B, Hq, Hkv, Nk_max, d, scale, num_splits, dt);
+  const fa_status st = check_decode(B, Hq, Hkv, Nk_max, d, scale, dt);
   if (st != FA_OK) return st;
   if (!aligned(q, 16) || !aligned(k8, 16) || !aligned(v8, 16) || !aligned(o, 16) || !aligned(workspace, 16) ||
       !aligned(k_scale, 4) || !aligned(v_scale, 4) || !aligned(seqlens_k, 4) || !aligned(lse, 4))
@@ -195,8 +224,7 @@ fa_status fa_decode_fp8(const void* q, const void* k8, const void* v8, const flo
   a.k_scale = k_scale;
   a.v_scale = v_scale;
   a.seqlens = seqlens_k;
-  a.o_part = static_cast<float*>(workspace);
-  a.lse_part = a.o_part + (size_t)B * Hq * num_splits * d;
+  place(a, workspace, workspace_of(B, Hq, Hkv, 0, d));
   a.o = o;
   a.lse = lse;
   a.B = B;
@@ -204,8 +232,7 @@ fa_status fa_decode_fp8(const void* q, const void* k8, const void* v8, const flo
   a.Hkv = Hkv;
   a.Nk_max = Nk_max;
   a.d = d;
-  a.num_splits = num_splits;
-  a.chunk = fa_decode_chunk(Nk_max, num_splits);
+  a.cache_ctas = cache_ctas_of(B, Hkv, Nk_max, d, Hq / Hkv, true, fa::device_sm_count(), 0);
   a.scale = scale;
   a.bf16 = dt == FA_BF16 ? 1 : 0;
   a.status = fa::device_status_word();
@@ -219,20 +246,28 @@ fa_status fa_decode_fp8(const void* q, const void* k8, const void* v8, const flo
 // Keys per prefix split: ceil(Np / splits) rounded up to a 128-key tile.
 static int prefix_chunk(int Np, int splits) { return ((Np + splits - 1) / splits + 127) / 128 * 128; }
 
-int fa_decode_prefix_splits(int B, int Hq, int Hkv, int Np, int num_sms) {
-  if (B < 1 || Hq < 1 || Hkv < 1 || Np < 1 || Hq % Hkv != 0 || Hq / Hkv > 128) return 1;
-  const int seqs = 128 / (Hq / Hkv);  // sequences per 128-row query tile, two tiles per CTA
-  const long long units = (long long)Hkv * ((B + 2 * seqs - 1) / (2 * seqs));
-  const int tiles = (Np + 127) / 128, sms = sm_count(num_sms);
-  // rounds of the SMs times a work's length in tiles, 3 of them for its start and end
+int fa_decode_prefix_splits(int B, int Hq, int Hkv, int Np, int Nk_max, int d, int fp8_cache, int num_sms) {
+  if (B < 1 || Hq < 1 || Hkv < 1 || Np < 1 || Nk_max < 0 || d < 1 || Hq % Hkv != 0 || Hq / Hkv > 128) return 1;
+  const int sms = sm_count(num_sms), tiles = (Np + 127) / 128;
+  const long long units = prefix_row_blocks(B, Hq / Hkv) * Hkv;
+  // Microseconds, as measured: a K/V tile takes 2 with two query tiles, 1.6 with one, a work 8 to start
+  // and end, and an SM streams 65 KB of cache.  The cache kernel fills the SMs that the prefix leaves, or
+  // follows it, which costs 8 and a third of its time more.  64 sequences behind 32768 keys, 1024 of
+  // their own: 10 splits (80 CTAs) 65 us, 18 (144) 79; 250 behind 8192, 512: 2 (64) 74 us, 4 (128) 87.
+  const double tile = B > 128 / (Hq / Hkv) ? 2.0 : 1.6;
+  const double cache = 2.0 * B * Nk_max * Hkv * (fp8_cache ? d + 4 : 2 * d) / 65e3;  // SM microseconds
   int best = 1;
-  long long cost = -1;
+  double least = -1;
   for (int s = 1; s <= std::min(tiles, 256); ++s) {
     const int per = (tiles + s - 1) / s;
     if ((tiles + per - 1) / per != s) continue;  // the same lengths with fewer splits
-    const long long c = ((units * s + sms - 1) / sms) * (per + 3);
-    if (cost < 0 || c < cost) {
-      cost = c;
+    const long long work = units * s;
+    const double prefix = (double)((work + sms - 1) / sms) * (per * tile + 8.0);
+    const double left = sms - (double)std::min<long long>(work, sms);
+    const double both = left >= sms / 4 ? std::max(prefix, cache / left) : prefix + 1.3 * cache / sms + 8.0;
+    const double cost = both + 0.1 * s;  // and every split a partial to merge
+    if (least < 0 || cost < least) {
+      least = cost;
       best = s;
     }
   }
@@ -242,12 +277,12 @@ int fa_decode_prefix_splits(int B, int Hq, int Hkv, int Np, int num_sms) {
 fa_status fa_decode_shared_prefix(const void* q, const void* k_prefix, const void* v_prefix, const void* k_cache,
                                   const void* v_cache, const float* k_scale, const float* v_scale,
                                   const int* seqlens_k, void* o, float* lse, void* workspace, int B, int Hq, int Hkv,
-                                  int Np, int Nk_max, int d, float scale, int prefix_splits, int num_splits,
+                                  int Np, int Nk_max, int d, float scale, int prefix_splits,
                                   fa_dtype dt, fa_stream_t stream) {
   if (!q || !k_prefix || !v_prefix || !k_cache || !v_cache || !seqlens_k || !o || !lse || !workspace)
     return FA_ERR_INVALID;
   if ((k_scale == nullptr) != (v_scale == nullptr)) return FA_ERR_INVALID;
-  const fa_status st = check_decode(B, Hq, Hkv, Nk_max, d, scale, num_splits, dt);
+  const fa_status st = check_decode(B, Hq, Hkv, Nk_max, d, scale, dt);
   if (st != FA_OK) return st;
   if (Np < 1 || prefix_splits < 1) return FA_ERR_INVALID;
   if (Np > (1 << 30) || prefix_splits > 65535) return FA_ERR_UNSUPPORTED;
@@ -268,8 +303,7 @@ fa_status fa_decode_shared_prefix(const void* q, const void* k_prefix, const voi
   a.k_scale = k_scale;
   a.v_scale = v_scale;
   a.seqlens = seqlens_k;
-  a.o_part = static_cast<float*>(workspace);
-  a.lse_part = a.o_part + (size_t)B * Hq * (prefix_splits + num_splits) * d;
+  place(a, workspace, workspace_of(B, Hq, Hkv, prefix_splits, d));
   a.o = o;
   a.lse = lse;
   a.B = B;
@@ -280,8 +314,9 @@ fa_status fa_decode_shared_prefix(const void* q, const void* k_prefix, const voi
   a.d = d;
   a.prefix_splits = prefix_splits;
   a.prefix_chunk = pchunk;
-  a.num_splits = num_splits;
-  a.chunk = fa_decode_chunk(Nk_max, num_splits);
+  const int sms = fa::device_sm_count();
+  const long long work = prefix_row_blocks(B, Hq / Hkv) * Hkv * prefix_splits;
+  a.cache_ctas = cache_ctas_of(B, Hkv, Nk_max, d, Hq / Hkv, k_scale != nullptr, sms, std::min<long long>(work, sms));
   a.scale = scale;
   a.bf16 = dt == FA_BF16 ? 1 : 0;
   a.status = fa::device_status_word();

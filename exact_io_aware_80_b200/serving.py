@@ -231,14 +231,12 @@ def fp8_cache_read(k8, v8, k_scale, v_scale, seqlens_k, Nk: int | None = None, d
 # decode
 # ---------------------------------------------------------------------------
 @functools.lru_cache(maxsize=1024)
-def _plan(device, B, Hq, Hkv, Np, Nk_max, d, prefix_splits, num_splits):
-    """Split counts (None: the library's suggestion) and workspace bytes: functions of the sizes alone."""
-    with _torch().cuda.device(device):
-        if prefix_splits is None:
-            prefix_splits = _lib.fa_decode_prefix_splits(B, Hq, Hkv, Np) if Np else 0
-        if num_splits is None:
-            num_splits = _lib.fa_decode_fp8_num_splits(B, Hkv, Nk_max)
-    return prefix_splits, num_splits, _lib.fa_decode_workspace_bytes(B, Hq, prefix_splits + num_splits, d)
+def _plan(device, B, Hq, Hkv, Np, Nk_max, d, fp8, prefix_splits):
+    """Prefix splits (None: the library's suggestion) and workspace bytes: functions of the sizes alone."""
+    if prefix_splits is None:
+        with _torch().cuda.device(device):
+            prefix_splits = _lib.fa_decode_prefix_splits(B, Hq, Hkv, Np, Nk_max, d, fp8)
+    return prefix_splits, _lib.fa_decode_fp8_workspace_bytes(B, Hq, Hkv, prefix_splits, d)
 
 
 def _decode_buffers(q, seqlens_k, need, workspace, out, lse):
@@ -264,25 +262,24 @@ def _decode_buffers(q, seqlens_k, need, workspace, out, lse):
     return workspace, out, lse
 
 
-def decode_fp8(q, k8, v8, k_scale, v_scale, seqlens_k, num_splits: int | None = None, scale: float | None = None,
-               workspace=None, out=None, lse=None):
+def decode_fp8(q, k8, v8, k_scale, v_scale, seqlens_k, scale: float | None = None, workspace=None, out=None,
+               lse=None):
     """One-token attention over an E4M3 cache; returns O [B, 1, Hq, d] and LSE [B, Hq, 1] (``fa_decode_fp8``)."""
     dt, dev = _dt(q), _device(q)
     B, _, Hq, d = q.shape
     Hkv = k8.shape[2]
     Nk_max = _check_cache(k8, v8, k_scale, v_scale, B, Hkv, d, dev)
     scale = 1.0 / math.sqrt(d) if scale is None else scale
-    _, num_splits, need = _plan(dev.index, B, Hq, Hkv, 0, Nk_max, d, None, num_splits)
+    _, need = _plan(dev.index, B, Hq, Hkv, 0, Nk_max, d, True, 0)
     workspace, out, lse = _decode_buffers(q, seqlens_k, need, workspace, out, lse)
     _call(dev, "fa_decode_fp8", q.data_ptr(), k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-          seqlens_k.data_ptr(), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), B, Hq, Hkv, Nk_max, d, scale,
-          num_splits, dt)
+          seqlens_k.data_ptr(), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), B, Hq, Hkv, Nk_max, d, scale, dt)
     return out, lse
 
 
 def decode_shared_prefix(q, k_prefix, v_prefix, k_cache, v_cache, seqlens_k, k_scale=None, v_scale=None,
-                         prefix_splits: int | None = None, num_splits: int | None = None, scale: float | None = None,
-                         workspace=None, out=None, lse=None):
+                         prefix_splits: int | None = None, scale: float | None = None, workspace=None, out=None,
+                         lse=None):
     """One-token attention of a batch behind one prefix; returns O [B, 1, Hq, d] and LSE [B, Hq, 1].
 
     Every sequence sees all of ``k_prefix``, ``v_prefix`` [1, Np, Hkv, d] and then the first
@@ -310,9 +307,9 @@ def decode_shared_prefix(q, k_prefix, v_prefix, k_cache, v_cache, seqlens_k, k_s
         _check("v_cache", v_cache, dtype, shape, dev)
         ksp = vsp = 0
     scale = 1.0 / math.sqrt(d) if scale is None else scale
-    prefix_splits, num_splits, need = _plan(dev.index, B, Hq, Hkv, Np, Nk_max, d, prefix_splits, num_splits)
+    prefix_splits, need = _plan(dev.index, B, Hq, Hkv, Np, Nk_max, d, bool(ksp), prefix_splits)
     workspace, out, lse = _decode_buffers(q, seqlens_k, need, workspace, out, lse)
     _call(dev, "fa_decode_shared_prefix", q.data_ptr(), k_prefix.data_ptr(), v_prefix.data_ptr(),
           k_cache.data_ptr(), v_cache.data_ptr(), ksp, vsp, seqlens_k.data_ptr(), out.data_ptr(), lse.data_ptr(),
-          workspace.data_ptr(), B, Hq, Hkv, Np, Nk_max, d, scale, prefix_splits, num_splits, dt)
+          workspace.data_ptr(), B, Hq, Hkv, Np, Nk_max, d, scale, prefix_splits, dt)
     return out, lse

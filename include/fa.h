@@ -413,24 +413,32 @@ fa_status fa_fp8_cache_read(const void* k8, const void* v8, const float* k_scale
                             const int* seqlens_k, void* k, void* v, int B, int Nk, int Hkv, int Nk_max, int d,
                             fa_dtype dt, fa_stream_t stream);
 
-/* Suggested number of key splits for fa_decode_fp8 (num_sms <= 0: query the current device). */
-int fa_decode_fp8_num_splits(int B, int Hkv, int Nk_max, int num_sms);
+/*
+ * Workspace bytes of fa_decode_fp8 (prefix_splits = 0) and fa_decode_shared_prefix:
+ * fp32 partials of B * Hq * prefix_splits rows and of at most B * Hkv + max(Hkv,
+ * 1024) pieces of the caches, Hq / Hkv rows each (0 on bad sizes).
+ */
+size_t fa_decode_fp8_workspace_bytes(int B, int Hq, int Hkv, int prefix_splits, int d);
 
 /*
  * One-token attention over an E4M3 cache (fa_fp8_cache_append): q [B,1,Hq,d] and
  * o [B,1,Hq,d] 16-bit (dt), lse [B,Hq,1] fp32; each sequence sees its first
  * seqlens_k[b] rows (DEVICE int32 [B], clamped into [0, Nk_max]); a sequence of
- * length 0 gets O = 0 and LSE = -inf.  The keys are cut into num_splits ranges
- * of fa_decode_chunk(Nk_max, num_splits) and merged by log-sum-exp; workspace
- * of fa_decode_workspace_bytes(B, Hq, num_splits, d) bytes.  scale >= 0, finite;
- * at most 16 query heads per KV head.  Scales in the cache are positive.
+ * length 0 gets O = 0 and LSE = -inf.  The keys that the lengths leave are shared
+ * out evenly among the CTAs and the pieces merged by log-sum-exp; workspace of
+ * fa_decode_fp8_workspace_bytes(B, Hq, Hkv, 0, d) bytes, 16-byte aligned.
+ * scale >= 0, finite; at most 16 query heads per KV head.  Scales in the cache
+ * are positive.
  */
 fa_status fa_decode_fp8(const void* q, const void* k8, const void* v8, const float* k_scale, const float* v_scale,
                         const int* seqlens_k, void* o, float* lse, void* workspace, int B, int Hq, int Hkv,
-                        int Nk_max, int d, float scale, int num_splits, fa_dtype dt, fa_stream_t stream);
+                        int Nk_max, int d, float scale, fa_dtype dt, fa_stream_t stream);
 
-/* Suggested number of prefix splits for fa_decode_shared_prefix (num_sms <= 0: query the current device). */
-int fa_decode_prefix_splits(int B, int Hq, int Hkv, int Np, int num_sms);
+/*
+ * Suggested number of prefix splits for fa_decode_shared_prefix, for caches of up to
+ * Nk_max keys in 16 bits or E4M3 (num_sms <= 0: query the current device).
+ */
+int fa_decode_prefix_splits(int B, int Hq, int Hkv, int Np, int Nk_max, int d, int fp8_cache, int num_sms);
 
 /*
  * One-token attention of a batch whose sequences share their first Np keys:
@@ -439,14 +447,14 @@ int fa_decode_prefix_splits(int B, int Hq, int Hkv, int Np, int num_sms);
  * k_cache, v_cache [B,Nk_max,Hkv,d]: 16-bit (dt) with k_scale and v_scale NULL,
  * or E4M3 codes with scales [B,Hkv,Nk_max].  q, o, lse, seqlens_k and limits as
  * fa_decode_fp8.  The prefix is cut into prefix_splits ranges of whole 128-key
- * tiles, none of them empty, the caches into num_splits; workspace of
- * fa_decode_workspace_bytes(B, Hq, prefix_splits + num_splits, d) bytes.
+ * tiles, none of them empty; workspace of
+ * fa_decode_fp8_workspace_bytes(B, Hq, Hkv, prefix_splits, d) bytes.
  */
 fa_status fa_decode_shared_prefix(const void* q, const void* k_prefix, const void* v_prefix, const void* k_cache,
                                   const void* v_cache, const float* k_scale, const float* v_scale,
                                   const int* seqlens_k, void* o, float* lse, void* workspace, int B, int Hq,
-                                  int Hkv, int Np, int Nk_max, int d, float scale, int prefix_splits,
-                                  int num_splits, fa_dtype dt, fa_stream_t stream);
+                                  int Hkv, int Np, int Nk_max, int d, float scale, int prefix_splits, fa_dtype dt,
+                                  fa_stream_t stream);
 
 /*
  * Synchronises `stream`, then reads and clears the device status word that the

@@ -257,24 +257,28 @@ def check_decode(q, k, v, lens, scale, o, lse, half_step, floor):
 F8_STEP, F8_FLOOR = 2.0 ** -11, 2.0 ** -25
 
 DECODE = [
-    # B, Hq, Hkv, N, d, dtype, splits, lens
-    (1, 1, 1, 1, 64, "fp16", None, [1]),
-    (1, 4, 4, 1, 128, "bf16", None, [1]),
-    (2, 16, 1, 65, 128, "bf16", None, [65, 64]),
-    (3, 14, 2, 200, 64, "bf16", 1, [200, 0, 63]),
-    (3, 14, 2, 200, 64, "fp16", 4, [200, 0, 129]),
-    (4, 8, 8, 1000, 128, "fp16", None, [1000, 1, 0, 513]),
-    (4, 8, 2, 1000, 128, "bf16", 3, [1000, 1, 0, 513]),
-    (2, 32, 8, 4099, 128, "bf16", None, [4099, 2050]),
-    (5, 3, 1, 777, 64, "bf16", 13, [777, 64, 65, 128, 600]),
+    # B, Hq, Hkv, N, d, dtype, lens
+    (1, 1, 1, 1, 64, "fp16", [1]),
+    (1, 4, 4, 1, 128, "bf16", [1]),
+    (2, 16, 1, 65, 128, "bf16", [65, 64]),
+    (3, 14, 2, 200, 64, "bf16", [200, 0, 63]),
+    (3, 14, 2, 200, 64, "fp16", [0, 0, 129]),
+    (4, 8, 8, 1000, 128, "fp16", [1000, 1, 0, 513]),
+    (4, 8, 2, 1000, 128, "bf16", [0, 1000, 128, 127]),
+    (2, 32, 8, 4099, 128, "bf16", [4099, 2050]),
+    (5, 3, 1, 777, 64, "bf16", [777, 64, 65, 128, 600]),
+    (1, 4, 1, 9000, 64, "fp16", [8999]),                       # one sequence over many CTAs
+    (300, 2, 2, 40, 64, "bf16", [b % 41 for b in range(300)]),  # many sequences to a CTA, more than threads
+    (140, 3, 3, 300, 128, "fp16", [(61 * b) % 301 if b % 3 else 0 for b in range(140)]),
+    (3, 5, 5, 70, 64, "bf16", [0, 0, 0]),
 ]
 
 
-@pytest.mark.parametrize("B,Hq,Hkv,N,d,dt,splits,lens", DECODE)
-def test_decode_fp8(fa, B, Hq, Hkv, N, d, dt, splits, lens):
+@pytest.mark.parametrize("B,Hq,Hkv,N,d,dt,lens", DECODE)
+def test_decode_fp8(fa, B, Hq, Hkv, N, d, dt, lens):
     q = normal((B, 1, Hq, d), DT[dt], 41)
     cache, k, v = filled_cache(fa, B, N, Hkv, d, lens, 42, spread=0.5)
-    o, lse = fa.decode_fp8(q.cuda(), *cache, ints(lens), splits)
+    o, lse = fa.decode_fp8(q.cuda(), *cache, ints(lens))
     done(fa)
     check_decode(q, k, v, lens, 1 / math.sqrt(d), o, lse, F8_STEP, F8_FLOOR)
 
@@ -327,19 +331,19 @@ def test_decode_fp8_passes_on_nan(fa):
 # decode behind a shared prefix
 # ---------------------------------------------------------------------------
 PREFIX = [
-    # B, Hq, Hkv, Np, Nk_max, d, dtype, fp8, prefix splits, cache splits
-    (1, 1, 1, 1, 1, 64, "fp16", False, None, None),
-    (1, 4, 2, 127, 3, 128, "bf16", True, None, None),
-    (3, 6, 2, 128, 70, 64, "bf16", False, None, None),      # G = 3: 42 sequences a tile, 126 rows
-    (4, 8, 2, 513, 64, 64, "fp16", False, None, None),
-    (2, 32, 2, 129, 65, 128, "bf16", True, 1, 2),           # G = 16
-    (32, 8, 2, 300, 40, 128, "fp16", True, 2, None),        # 128 rows: one full tile
-    (33, 8, 2, 300, 40, 128, "bf16", False, None, None),    # 132 rows: the second tile holds one sequence
-    (64, 4, 1, 1000, 20, 64, "bf16", True, 3, 1),           # 256 rows
-    (65, 8, 2, 640, 20, 128, "bf16", False, 5, 1),          # 260 rows: a second row block
-    (53, 5, 1, 400, 33, 64, "fp16", True, None, None),      # G = 5: 25 sequences a tile
-    (150, 1, 1, 257, 5, 128, "bf16", False, None, None),    # G = 1
-    (40, 14, 2, 260, 9, 64, "bf16", False, 1, None),        # G = 7: 18 sequences a tile, 126 rows
+    # B, Hq, Hkv, Np, Nk_max, d, dtype, fp8, prefix splits
+    (1, 1, 1, 1, 1, 64, "fp16", False, None),
+    (1, 4, 2, 127, 3, 128, "bf16", True, None),
+    (3, 6, 2, 128, 70, 64, "bf16", False, None),      # G = 3: 42 sequences a tile, 126 rows
+    (4, 8, 2, 513, 64, 64, "fp16", False, None),
+    (2, 32, 2, 129, 65, 128, "bf16", True, 1),           # G = 16
+    (32, 8, 2, 300, 40, 128, "fp16", True, 2),        # 128 rows: one full tile
+    (33, 8, 2, 300, 40, 128, "bf16", False, None),    # 132 rows: the second tile holds one sequence
+    (64, 4, 1, 1000, 20, 64, "bf16", True, 3),           # 256 rows
+    (65, 8, 2, 640, 20, 128, "bf16", False, 5),          # 260 rows: a second row block
+    (53, 5, 1, 400, 33, 64, "fp16", True, None),      # G = 5: 25 sequences a tile
+    (150, 1, 1, 257, 5, 128, "bf16", False, None),    # G = 1
+    (40, 14, 2, 260, 9, 64, "bf16", False, 1),        # G = 7: 18 sequences a tile, 126 rows
 ]
 
 
@@ -361,11 +365,11 @@ def prefix_case(fa, B, Hq, Hkv, Np, Nk, d, dt, fp8, lens, seed):
     return q, args, k, v
 
 
-@pytest.mark.parametrize("B,Hq,Hkv,Np,Nk,d,dt,fp8,ps,cs", PREFIX)
-def test_decode_shared_prefix(fa, B, Hq, Hkv, Np, Nk, d, dt, fp8, ps, cs):
+@pytest.mark.parametrize("B,Hq,Hkv,Np,Nk,d,dt,fp8,ps", PREFIX)
+def test_decode_shared_prefix(fa, B, Hq, Hkv, Np, Nk, d, dt, fp8, ps):
     lens = [(7 * b + Nk) % (Nk + 1) for b in range(B)]  # 0 among them
     q, args, k, v = prefix_case(fa, B, Hq, Hkv, Np, Nk, d, dt, fp8, lens, 51)
-    o, lse = fa.decode_shared_prefix(*args, prefix_splits=ps, num_splits=cs)
+    o, lse = fa.decode_shared_prefix(*args, prefix_splits=ps)
     done(fa)
     # weights in q's type (half a step of it, 2^-25 absolute in fp16) or in fp16
     check_decode(q, k, v, [Np + n for n in lens], 1 / math.sqrt(d), o, lse,
@@ -447,7 +451,7 @@ def test_decode_refusals(fa):
     with pytest.raises(fa.FAError):
         fa.decode_fp8(q, *cache, lens, scale=float("inf"))
     with pytest.raises(fa.FAError):
-        fa.decode_fp8(q, *cache, lens, num_splits=2)
+        fa.decode_shared_prefix(q, kp, kp, cache[0], cache[1], lens, cache[2], cache[3], prefix_splits=2)
     done(fa)
 
 
@@ -529,8 +533,8 @@ def test_graphs_that_share_a_workspace_and_other_streams(fa):
     q = [normal((B, 1, Hq, d), torch.bfloat16, 102 + i).cuda() for i in range(2)]
     kp, vp = (normal((1, 333, Hkv, d), torch.bfloat16, 104 + i).cuda() for i in range(2))
     sl = ints(lens)
-    S, P = fa.fa_decode_fp8_num_splits(B, Hkv, N), fa.fa_decode_prefix_splits(B, Hq, Hkv, 333)
-    ws = torch.empty(fa.fa_decode_workspace_bytes(B, Hq, S + P, d), dtype=torch.uint8, device="cuda")
+    P = fa.fa_decode_prefix_splits(B, Hq, Hkv, 333, N, d, True)
+    ws = torch.empty(fa.fa_decode_fp8_workspace_bytes(B, Hq, Hkv, P, d), dtype=torch.uint8, device="cuda")
 
     def a():
         return fa.decode_fp8(q[0], *cache, sl, workspace=ws)

@@ -67,24 +67,24 @@ def test_cache_read_rejects_bad_arguments(lib):
 
 
 def test_decode_fp8_rejects_bad_arguments(lib):
-    # q, k8, v8, ks, vs, seqlens, o, lse, ws, B, Hq, Hkv, Nk_max, d, scale, splits, dt, stream
-    base = [FAKE] * 9 + [2, 32, 8, 1024, 128, 0.1, 4, 1, None]
+    # q, k8, v8, ks, vs, seqlens, o, lse, ws, B, Hq, Hkv, Nk_max, d, scale, dt, stream
+    base = [FAKE] * 9 + [2, 32, 8, 1024, 128, 0.1, 1, None]
     _rejects(lib.fa_decode_fp8, base, [
-        ({0: 0}, -1), ({3: 0}, -1), ({8: 0}, -1), ({10: 33}, -1), ({9: 0}, -1), ({12: 0}, -1), ({15: 0}, -1),
-        ({15: 17}, -1), ({14: -0.1}, -1), ({14: math.inf}, -1), ({14: math.nan}, -1),
-        ({10: 64, 11: 2}, -2), ({13: 96}, -2), ({16: 3}, -2), ({9: 65536}, -2), ({12: (1 << 30) + 1}, -2),
+        ({0: 0}, -1), ({3: 0}, -1), ({8: 0}, -1), ({10: 33}, -1), ({9: 0}, -1), ({12: 0}, -1),
+        ({14: -0.1}, -1), ({14: math.inf}, -1), ({14: math.nan}, -1),
+        ({10: 64, 11: 2}, -2), ({13: 96}, -2), ({15: 3}, -2), ({9: 65536}, -2), ({12: (1 << 30) + 1}, -2),
         ({1: FAKE + 8}, -3), ({4: FAKE + 2}, -3), ({5: FAKE + 2}, -3), ({7: FAKE + 2}, -3), ({8: FAKE + 8}, -3),
     ])
 
 
 def test_decode_shared_prefix_rejects_bad_arguments(lib):
-    # q, kp, vp, kc, vc, ks, vs, seqlens, o, lse, ws, B, Hq, Hkv, Np, Nk_max, d, scale, psplits, splits, dt, stream
-    base = [FAKE] * 5 + [0, 0] + [FAKE] * 4 + [2, 32, 8, 1000, 1024, 128, 0.1, 4, 4, 1, None]
+    # q, kp, vp, kc, vc, ks, vs, seqlens, o, lse, ws, B, Hq, Hkv, Np, Nk_max, d, scale, psplits, dt, stream
+    base = [FAKE] * 5 + [0, 0] + [FAKE] * 4 + [2, 32, 8, 1000, 1024, 128, 0.1, 4, 1, None]
     _rejects(lib.fa_decode_shared_prefix, base, [
         ({0: 0}, -1), ({1: 0}, -1), ({4: 0}, -1), ({10: 0}, -1), ({5: FAKE}, -1), ({6: FAKE}, -1), ({12: 33}, -1),
-        ({14: 0}, -1), ({15: 0}, -1), ({18: 0}, -1), ({18: 9}, -1), ({19: 0}, -1), ({19: 17}, -1), ({17: -1.0}, -1),
+        ({14: 0}, -1), ({15: 0}, -1), ({18: 0}, -1), ({18: 9}, -1), ({17: -1.0}, -1),
         ({14: 1200, 18: 9}, -1),  # nine splits of two tiles: the last four would be empty
-        ({12: 64, 13: 2}, -2), ({16: 96}, -2), ({20: 2}, -2), ({14: (1 << 30) + 1}, -2),
+        ({12: 64, 13: 2}, -2), ({16: 96}, -2), ({19: 2}, -2), ({14: (1 << 30) + 1}, -2),
         ({2: FAKE + 8}, -3), ({7: FAKE + 2}, -3), ({5: FAKE + 2, 6: FAKE}, -3), ({10: FAKE + 4}, -3),
     ])
 
@@ -93,11 +93,14 @@ def test_split_plans_are_accepted_shapes(lib):
     from exact_io_aware_80_b200 import _lib
     for B, Hkv, G in ((1, 1, 1), (4, 2, 4), (64, 8, 4), (250, 8, 4), (33, 3, 7), (9, 16, 16)):
         for N in (1, 64, 127, 128, 129, 513, 4096, 12345, 100000):
-            s = _lib.fa_decode_prefix_splits(B, Hkv * G, Hkv, N, 148)
-            chunk = -(-(-(-N // s)) // 128) * 128
-            assert 1 <= s <= -(-N // 128) and (s - 1) * chunk < N
-            s = _lib.fa_decode_fp8_num_splits(B, Hkv, N, 148)
-            assert 1 <= s <= -(-N // 64) and (s - 1) * _lib.fa_decode_chunk(N, s) < N
+            for Nk, fp8 in ((1, 0), (1000, 1), (30000, 0)):
+                s = _lib.fa_decode_prefix_splits(B, Hkv * G, Hkv, N, Nk, 128, fp8, 148)
+                chunk = -(-(-(-N // s)) // 128) * 128
+                assert 1 <= s <= -(-N // 128) and (s - 1) * chunk < N
+    ws = _lib.fa_decode_fp8_workspace_bytes
+    assert ws(2, 8, 2, 0, 128) >= (2 * 2 + 1024) * 4 * 129 * 4 + 2 * 8
+    assert ws(2, 8, 2, 3, 64) - ws(2, 8, 2, 0, 64) >= 2 * 8 * 3 * 65 * 4
+    assert ws(2, 8, 3, 0, 64) == 0 and ws(0, 8, 2, 0, 64) == 0 and ws(2, 8, 2, -1, 64) == 0
 
 
 # ---------------------------------------------------------------------------
