@@ -62,6 +62,12 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr float kStale = 6.f;  // log2 units that a score may exceed the reference m by
+// Rounding the weights to 16 bits costs an output as much as its own rounding does: over many outputs
+// 1.41 times the error of the last rounding alone, over the few of a small batch up to 1.6.  With REST
+// the rounding errors are multiplied too, and only the last rounding shows.  A 16-bit cache always takes
+// it (its loads hide it); an E4M3 cache with bf16 output never (its weights are rounded to fp16), with
+// fp16 output up to so many rows (32 sequences of 3000 keys, 16 heads, d = 64: 39.6 us with, 33.6 without).
+constexpr int kRestRows = 256;
 constexpr int kMinUnit = -112;  // smallest e of the weights' unit (all powers of two below stay normal)
 
 // A warp's two buffers of kStep keys each.  Two of them (99 KB in flight on an SM of three CTAs) leave
@@ -127,7 +133,7 @@ struct Item {
   int blk, blks;     // that block within the sequence, and the sequence's blocks
 };
 
-template <typename T, int D, bool F8, int NB>
+template <typename T, int D, bool F8, int NB, bool REST>
 __global__ void __launch_bounds__(kThreads, cache_ctas_per_sm(D, F8, NB == 2)) cache_decode_kernel(CacheDecodeArgs p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   using R = Ring<D, F8>;
@@ -137,8 +143,9 @@ __global__ void __launch_bounds__(kThreads, cache_ctas_per_sm(D, F8, NB == 2)) c
   constexpr int kBlock = 4 * R::kStep;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = p.Hq / p.Hkv, hk = blockIdx.x % p.Hkv, cta = blockIdx.x / p.Hkv;
-  // the merge, launched next as a programmatic dependent, may become resident; it waits for this
-  // grid's end before it reads a partial
+  // behind every earlier grid but a prefix kernel's, which itself started behind all others; the merge,
+  // launched next, may become resident
+  if (!p.after_prefix) asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   const uint32_t ring = smem_u32(smem) + warp * 2 * R::kStage;
@@ -455,7 +462,8 @@ __global__ void __launch_bounds__(kThreads, cache_ctas_per_sm(D, F8, NB == 2)) c
             for (int e = 0; e < 4; ++e) acc[nb][k][e] *= corr[e & 1];
         }
       }
-      uint32_t pb[MB][NB][2];  // P^T as B fragments
+      // P^T as B fragments, and (REST) what their rounding left
+      uint32_t pb[MB][NB][2], pr[MB][NB][2];
 #pragma unroll
       for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
@@ -468,7 +476,13 @@ __global__ void __launch_bounds__(kThreads, cache_ctas_per_sm(D, F8, NB == 2)) c
             const float p0 = ex2(sc[mb][nb][2 * e] - mu0), p1 = ex2(sc[mb][nb][2 * e + 1] - mu1);
             l[nb][0] += p0;
             l[nb][1] += p1;
-            pb[mb][nb][e] = transpose8(Elem<M>::pack(F8 ? p0 * vf : p0, F8 ? p1 * vf : p1));
+            const float w0 = F8 ? p0 * vf : p0, w1 = F8 ? p1 * vf : p1;
+            const uint32_t hi = Elem<M>::pack(w0, w1);
+            pb[mb][nb][e] = transpose8(hi);
+            if constexpr (REST) {
+              const float2 h = Elem<M>::unpack(hi);
+              pr[mb][nb][e] = transpose8(Elem<M>::pack(w0 - h.x, w1 - h.y));
+            }
           }
         }
 #pragma unroll
@@ -484,7 +498,10 @@ __global__ void __launch_bounds__(kThreads, cache_ctas_per_sm(D, F8, NB == 2)) c
               e4m3x4_to_h2(__byte_perm(r[2 * h], 0, 0x3120), a[0], a[1]);
               e4m3x4_to_h2(__byte_perm(r[2 * h + 1], 0, 0x3120), a[2], a[3]);
 #pragma unroll
-              for (int nb = 0; nb < NB; ++nb) mma16816<M>(acc[nb][k + h], a, pb[mb][nb][0], pb[mb][nb][1]);
+              for (int nb = 0; nb < NB; ++nb) {
+                mma16816<M>(acc[nb][k + h], a, pb[mb][nb][0], pb[mb][nb][1]);
+                if constexpr (REST) mma16816<M>(acc[nb][k + h], a, pr[mb][nb][0], pr[mb][nb][1]);
+              }
             }
           }
         } else {
@@ -494,7 +511,10 @@ __global__ void __launch_bounds__(kThreads, cache_ctas_per_sm(D, F8, NB == 2)) c
             ldsm_x4_t(st + R::kTile + chunk_at<R::kRow>(16 * mb + (lane & 7) + 8 * (lane >> 4), 2 * k + ((lane >> 3) & 1)),
                       a[0], a[1], a[2], a[3]);
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) mma16816<M>(acc[nb][k], a, pb[mb][nb][0], pb[mb][nb][1]);
+            for (int nb = 0; nb < NB; ++nb) {
+              mma16816<M>(acc[nb][k], a, pb[mb][nb][0], pb[mb][nb][1]);
+              if constexpr (REST) mma16816<M>(acc[nb][k], a, pr[mb][nb][0], pr[mb][nb][1]);
+            }
           }
         }
       }
@@ -563,9 +583,8 @@ __global__ void __launch_bounds__(kThreads, cache_ctas_per_sm(D, F8, NB == 2)) c
     have = more;
   }
   cp_async_wait<0>();
-  // launched as a programmatic dependent of the prefix kernel: this grid must not end before that
-  // one has, since the merge waits only for this one (without the launch attribute the wait
-  // returns at once)
+  // after a prefix kernel this grid must not end before that one has, since the merge waits only for
+  // this one
   if (blockIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
@@ -584,6 +603,8 @@ __global__ void __launch_bounds__(combine_threads(WARPS)) cache_combine_kernel(C
   const int Sp = p.prefix_splits, G = p.Hq / p.Hkv;
   const int b = (int)(row / p.Hq), h = (int)(row - (long)b * p.Hq), hk = h / G;
   const bool has = row < nrows && p.seqlens[row < nrows ? b : 0] > 0 && p.Nk_max > 0;
+  // (no early start for what follows: the next pass's CTAs, taking their places among this kernel's,
+  // came to lie unevenly on the SMs and cost 3 % of a long decode)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int2 span = has ? p.spans[b] : make_int2(0, -1);
   const int live = row < nrows ? Sp + span.y - span.x + 1 : 0;
@@ -645,32 +666,27 @@ __global__ void __launch_bounds__(combine_threads(WARPS)) cache_combine_kernel(C
   if (lane == 0) p.lse[row] = mu + logf(l);
 }
 
-template <typename T, int D, bool F8, int NB>
-cudaError_t launch_part(const CacheDecodeArgs& a, int after_prefix, cudaStream_t s) {
-  auto kern = cache_decode_kernel<T, D, F8, NB>;
+template <typename T, int D, bool F8, int NB, bool REST>
+cudaError_t launch_part(const CacheDecodeArgs& a, cudaStream_t s) {
+  auto kern = cache_decode_kernel<T, D, F8, NB, REST>;
   constexpr int smem = Smem<D, F8, NB>::kBytes;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(a.cache_ctas);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  if (after_prefix) {
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-  }
-  return cudaLaunchKernelEx(&cfg, kern, a);
+  return launch_dependent(kern, dim3(a.cache_ctas), kThreads, smem, s, a);
 }
 
+template <typename T, int D, bool F8, bool REST>
+cudaError_t launch_part_w(const CacheDecodeArgs& a, cudaStream_t s) {
+  // groups of 9 to 16 query heads take two column blocks
+  return a.Hq / a.Hkv > 8 ? launch_part<T, D, F8, 2, REST>(a, s) : launch_part<T, D, F8, 1, REST>(a, s);
+}
 template <typename T, int D>
-cudaError_t launch_part_d(const CacheDecodeArgs& a, int after_prefix, cudaStream_t s) {
-  const bool wide = a.Hq / a.Hkv > 8;  // groups of 9 to 16 query heads take two column blocks
-  if (a.k_scale) return wide ? launch_part<T, D, true, 2>(a, after_prefix, s) : launch_part<T, D, true, 1>(a, after_prefix, s);
-  return wide ? launch_part<T, D, false, 2>(a, after_prefix, s) : launch_part<T, D, false, 1>(a, after_prefix, s);
+cudaError_t launch_part_d(const CacheDecodeArgs& a, cudaStream_t s) {
+  if (!a.k_scale) return launch_part_w<T, D, false, true>(a, s);
+  if constexpr (!Elem<T>::kBf16) {
+    if (a.B * (long)a.Hq <= kRestRows) return launch_part_w<T, D, true, true>(a, s);
+  }
+  return launch_part_w<T, D, true, false>(a, s);
 }
 
 template <typename T, int D>
@@ -682,29 +698,19 @@ cudaError_t launch_combine(const CacheDecodeArgs& a, cudaStream_t s) {
   const int per = combine_threads(warps) / 32 / warps;  // rows a CTA
   const long ctas = (rows + per - 1) / per;
   if (ctas > 0x7fffffffL) return cudaErrorInvalidValue;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)ctas);
-  cfg.blockDim = dim3(combine_threads(warps));
-  cfg.stream = s;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg,
-                            warps == 16 ? cache_combine_kernel<T, D, 16>
-                            : warps == 4 ? cache_combine_kernel<T, D, 4>
-                                         : cache_combine_kernel<T, D, 1>,
-                            a);
+  auto kern = warps == 16 ? cache_combine_kernel<T, D, 16>
+              : warps == 4 ? cache_combine_kernel<T, D, 4>
+                           : cache_combine_kernel<T, D, 1>;
+  return launch_dependent(kern, dim3((unsigned)ctas), combine_threads(warps), 0, s, a);
 }
 
 }  // namespace
 
-cudaError_t launch_cache_decode(const CacheDecodeArgs& a, int after_prefix, cudaStream_t s) {
+cudaError_t launch_cache_decode(const CacheDecodeArgs& a, cudaStream_t s) {
   if (a.bf16)
-    return a.d == 128 ? launch_part_d<__nv_bfloat16, 128>(a, after_prefix, s)
-                      : launch_part_d<__nv_bfloat16, 64>(a, after_prefix, s);
-  return a.d == 128 ? launch_part_d<__half, 128>(a, after_prefix, s) : launch_part_d<__half, 64>(a, after_prefix, s);
+    return a.d == 128 ? launch_part_d<__nv_bfloat16, 128>(a, s)
+                      : launch_part_d<__nv_bfloat16, 64>(a, s);
+  return a.d == 128 ? launch_part_d<__half, 128>(a, s) : launch_part_d<__half, 64>(a, s);
 }
 
 cudaError_t launch_cache_combine(const CacheDecodeArgs& a, cudaStream_t s) {

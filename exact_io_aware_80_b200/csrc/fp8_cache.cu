@@ -84,6 +84,7 @@ __device__ __forceinline__ uint4 codes16(const float (&x)[16], float s) {
 // grid: (row groups, 2); y = 0 appends K rows, 1 V rows.  D / 16 consecutive threads hold a row.
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) append_kernel(Fp8CacheArgs p, Rows rows) {
+  wait_for_earlier_grids();
   constexpr int kUnits = D / 16;
   const bool isv = blockIdx.y != 0;
   const uint32_t r = blockIdx.x * (kThreads / kUnits) + threadIdx.x / kUnits;
@@ -155,6 +156,7 @@ __device__ __forceinline__ void decode16(const uint4 c, float s, uint4 (&out)[2]
 constexpr int kReadRows = 2;
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) read_kernel(Fp8CacheArgs p, Rows rows) {
+  wait_for_earlier_grids();
   constexpr int kUnits = D / 16, kPer = kThreads / kUnits;
   const bool isv = blockIdx.y != 0;
   const uint32_t r0 = blockIdx.x * (kPer * kReadRows) + threadIdx.x / kUnits;
@@ -199,15 +201,13 @@ template <typename T, int D>
 cudaError_t launch_append(const Fp8CacheArgs& a, cudaStream_t s) {
   const Rows rows = rows_of(a);
   const uint32_t per = kThreads / (D / 16);
-  append_kernel<T, D><<<dim3((rows.count + per - 1) / per, 2), kThreads, 0, s>>>(a, rows);
-  return cudaGetLastError();
+  return launch_dependent(append_kernel<T, D>, dim3((rows.count + per - 1) / per, 2), kThreads, 0, s, a, rows);
 }
 template <typename T, int D>
 cudaError_t launch_read(const Fp8CacheArgs& a, cudaStream_t s) {
   const Rows rows = rows_of(a);
   const uint32_t per = kThreads / (D / 16) * kReadRows;
-  read_kernel<T, D><<<dim3((rows.count + per - 1) / per, 2), kThreads, 0, s>>>(a, rows);
-  return cudaGetLastError();
+  return launch_dependent(read_kernel<T, D>, dim3((rows.count + per - 1) / per, 2), kThreads, 0, s, a, rows);
 }
 
 }  // namespace

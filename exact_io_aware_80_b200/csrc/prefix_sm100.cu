@@ -47,6 +47,7 @@ using namespace sm100;
 constexpr int kBM = 128;     // rows of a query tile (= TMEM lanes)
 constexpr int kBN = 128;     // keys per K/V tile
 constexpr int kStages = 2;   // K/V ring depth
+constexpr int kRestRows = 32;  // up to so many query rows of a KV head P is taken as two 16-bit values
 // Register split with two query tiles: launched at 168 per thread (384 x 168 = 64512), the
 // load/MMA warpgroup drops to 104 and the softmax warpgroups rise to 200 (2 x 128 x 200 +
 // 128 x 104 = 64512).  One query tile (256 threads) needs no split.
@@ -87,7 +88,7 @@ __device__ __forceinline__ float2 exp2_pair(float2 x, int pair) {
   return make_float2(ex2(x.x), ex2(x.y));
 }
 
-template <int D, int NT>
+template <int D, int NT, bool REST>
 struct Smem {
   static constexpr int kPanel = 128 * 128;  // one [128 rows][128 bytes] swizzled panel
   static constexpr int kTile = (D / 64) * kPanel;
@@ -107,6 +108,7 @@ struct Smem {
   static constexpr int kThreads = 128 * (NT + 1);
   static constexpr int kHalves = NT == 1 ? 2 : 1;  // S buffers of a query tile
   static constexpr int kWidth = kBN / kHalves;     // their keys
+  static_assert(!REST || kHalves == 2, "the rest of P lies in the free half of an S buffer's columns");
   // TMEM columns: S_t, then O_t
   static constexpr uint32_t col_s(int t) { return 128u * t; }
   static constexpr uint32_t col_o(int t) { return 128u * NT + 128u * t; }
@@ -132,11 +134,11 @@ __device__ __forceinline__ Work work_at(const Params& p, int w) {
   return Work{w % p.row_blocks, (w / p.row_blocks) % p.Hkv, w / (p.row_blocks * p.Hkv)};
 }
 
-template <typename T, int D, int NT>
-__global__ void __launch_bounds__(Smem<D, NT>::kThreads, 1)
+template <typename T, int D, int NT, bool REST>
+__global__ void __launch_bounds__(Smem<D, NT, REST>::kThreads, 1)
     prefix_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                         const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO, Params p) {
-  using L = Smem<D, NT>;
+  using L = Smem<D, NT, REST>;
   constexpr int kWarpLoad = 4 * NT, kWarpMma = 4 * NT + 1;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -146,9 +148,6 @@ __global__ void __launch_bounds__(Smem<D, NT>::kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(gb + L::kOffAbort);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  // the cache's partials, launched next as a programmatic dependent, share no memory with this
-  // kernel's and may fill SMs as its CTAs leave
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   auto blocks_of = [&](const Work& x) {  // K/V tiles of a split
     return (min(p.chunk, p.Np - x.s * p.chunk) + kBN - 1) / kBN;
   };
@@ -170,6 +169,9 @@ __global__ void __launch_bounds__(Smem<D, NT>::kThreads, 1)
     prefetch_tmap(&tmV);
     prefetch_tmap(&tmO);
   }
+  // behind every earlier grid; and the caches' partials, launched next as a programmatic dependent,
+  // share no output with this kernel and may fill SMs as its CTAs leave
+  wait_for_earlier_grids();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -255,6 +257,8 @@ __global__ void __launch_bounds__(Smem<D, NT>::kThreads, 1)
           const uint64_t bd =
               sdesc_sw128(sb + L::kOffV + st * L::kTile + (h * (L::kWidth / 16) + kk) * 2048, L::kPanel, 1024);
           mma_ts(tbase + L::col_o(t), tbase + L::col_s(t) + L::kWidth * h + kk * 8, bd, idv, (!first || kk > 0) ? 1u : 0u);
+          if constexpr (REST)  // and what rounding P left, in the second half of S's columns
+            mma_ts(tbase + L::col_o(t), tbase + L::col_s(t) + L::kWidth * h + L::kWidth / 2 + kk * 8, bd, idv, 1u);
         }
       };
       bool ok = true;
@@ -379,7 +383,7 @@ __global__ void __launch_bounds__(Smem<D, NT>::kThreads, 1)
           float2 rs0 = make_float2(0.f, 0.f), rs1 = make_float2(0.f, 0.f);
 #pragma unroll
           for (int q = 0; q < L::kWidth / 32; ++q) {
-            uint32_t pk[16];
+            uint32_t pk[16], pr[16];
 #pragma unroll
             for (int i = 0; i < 16; i += 2) {
               const int c0 = 32 * q + 2 * i;
@@ -390,8 +394,14 @@ __global__ void __launch_bounds__(Smem<D, NT>::kThreads, 1)
               rs1 = __fadd2_rn(rs1, bb);
               pk[i] = Elem<T>::pack(a.x, a.y);
               pk[i + 1] = Elem<T>::pack(bb.x, bb.y);
+              if constexpr (REST) {
+                const float2 ha = Elem<T>::unpack(pk[i]), hb = Elem<T>::unpack(pk[i + 1]);
+                pr[i] = Elem<T>::pack(a.x - ha.x, a.y - ha.y);
+                pr[i + 1] = Elem<T>::pack(bb.x - hb.x, bb.y - hb.y);
+              }
             }
             tmem_st16(tSh + 16 * q, pk);
+            if constexpr (REST) tmem_st16(tSh + L::kWidth / 2 + 16 * q, pr);
           }
           l += (rs0.x + rs0.y) + (rs1.x + rs1.y);
           // a NaN or +inf score makes the row NaN, also where the polynomial would clamp it away
@@ -486,7 +496,7 @@ __global__ void __launch_bounds__(Smem<D, NT>::kThreads, 1)
   }
 }
 
-template <typename T, int D, int NT>
+template <typename T, int D, int NT, bool REST>
 cudaError_t launch(const CacheDecodeArgs& a, cudaStream_t s) {
   const int G = a.Hq / a.Hkv, seqs = kBM / G, S = a.prefix_splits;
   const int type = Elem<T>::kBf16 ? kMapBf16 : kMapF16;
@@ -511,20 +521,27 @@ cudaError_t launch(const CacheDecodeArgs& a, cudaStream_t s) {
   if (work > (1ll << 30)) return cudaErrorInvalidValue;
   Params p{a.lse_part, a.B, a.Hq, a.Hkv, a.Np, G, seqs, S, a.prefix_chunk, rows, (int)work,
            a.scale * kLog2e, a.status};
-  auto kern = prefix_sm100_kernel<T, D, NT>;
-  constexpr int smem = Smem<D, NT>::kBytes;
+  auto kern = prefix_sm100_kernel<T, D, NT, REST>;
+  constexpr int smem = Smem<D, NT, REST>::kBytes;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const int grid = (int)std::min<long long>(work, device_sm_count());
-  kern<<<grid, Smem<D, NT>::kThreads, smem, s>>>(mq, mk, mv, mo, p);
-  return cudaGetLastError();
+  return launch_dependent(kern, dim3(grid), Smem<D, NT, REST>::kThreads, smem, s, mq, mk, mv, mo, p);
+}
+
+template <typename T, int D>
+cudaError_t launch_d(const CacheDecodeArgs& a, cudaStream_t s) {
+  const int G = a.Hq / a.Hkv;
+  if (a.B > kBM / G) return launch<T, D, 2, false>(a, s);
+  // Every sequence fits one query tile.  Rounding P to 16 bits costs an output as much as its own
+  // rounding does: over many outputs 1.41 times the error of the last rounding alone, over the few of
+  // a small batch up to 1.6.  There P's rest is multiplied too (1.83 us a K/V tile instead of 1.57).
+  return a.B * G <= kRestRows ? launch<T, D, 1, true>(a, s) : launch<T, D, 1, false>(a, s);
 }
 
 template <typename T>
 cudaError_t launch_t(const CacheDecodeArgs& a, cudaStream_t s) {
-  const bool one = (long)a.B <= kBM / (a.Hq / a.Hkv);  // every sequence fits one query tile
-  if (a.d == 128) return one ? launch<T, 128, 1>(a, s) : launch<T, 128, 2>(a, s);
-  return one ? launch<T, 64, 1>(a, s) : launch<T, 64, 2>(a, s);
+  return a.d == 128 ? launch_d<T, 128>(a, s) : launch_d<T, 64>(a, s);
 }
 
 }  // namespace

@@ -106,6 +106,7 @@ template <typename T, int D, bool INTER, int BATCH>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(Params p) {
   constexpr int kUnits = D / 16;     // threads per head, 16 values each
   constexpr int kRow = 32 / kUnits;  // heads per warp and step
+  wait_for_earlier_grids();
   const int lane = threadIdx.x & 31;
   const uint32_t tok = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
   if (tok >= p.tokens) return;
@@ -176,8 +177,7 @@ cudaError_t launch(const RotaryArgs& a, Params p, cudaStream_t s) {
   const int rows = (int)std::min<long>(steps, std::max<long>(1, want / groups));
   p.per_y = (steps + rows - 1) / rows * (kRow * kBatch);
   const dim3 grid(groups, (H + p.per_y - 1) / p.per_y);
-  rotary_kernel<T, D, INTER, kBatch><<<grid, kThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  return launch_dependent(rotary_kernel<T, D, INTER, kBatch>, grid, kThreads, 0, s, p);
 }
 
 template <typename T, int D>

@@ -7,6 +7,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <utility>
+
 namespace fa {
 
 // Device status word of the current device (fa_api.cu), nullptr if it cannot be found.
@@ -31,6 +33,31 @@ struct FastDiv {
   __device__ __forceinline__ uint32_t operator()(uint32_t n) const { return (__umulhi(n, m) + n) >> l; }
 #endif
 };
+
+// Launch as a programmatic dependent of whatever precedes on the stream: the grid may become
+// resident before that has finished, and orders itself behind it (and behind all before it) with
+// griddepcontrol.wait ahead of its first access to global memory.
+template <typename... Params, typename... Args>
+cudaError_t launch_dependent(void (*kern)(Params...), dim3 grid, int threads, int smem, cudaStream_t s, Args&&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
+}
+#ifdef __CUDACC__
+// Behind every earlier grid, and then: the next one may become resident.
+__device__ __forceinline__ void wait_for_earlier_grids() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+#endif
 
 // Rotary positions of q [B,N,Hq,d] and k [B,N,Hkv,d] (rotary.cu).  Input strides in elements
 // (heads are d apart); outputs contiguous, or the inputs themselves.
@@ -88,14 +115,15 @@ struct CacheDecodeArgs {
   float* lse;
   int B, Hq, Hkv, Np, Nk_max, d;
   int prefix_splits, prefix_chunk;  // keys per prefix split, a multiple of 128
+  int after_prefix;                 // the launch before the cache kernel's is the prefix kernel's
   int cache_ctas;                   // a multiple of Hkv, at most max(kMaxCacheCtas, Hkv)
   float scale;
   int bf16;
   int* status;
 };
 cudaError_t launch_prefix_sm100(const CacheDecodeArgs& a, cudaStream_t s);
-// The cache's partials; `after_prefix`: the previous launch on the stream is launch_prefix_sm100.
-cudaError_t launch_cache_decode(const CacheDecodeArgs& a, int after_prefix, cudaStream_t s);
+// The caches' partials.
+cudaError_t launch_cache_decode(const CacheDecodeArgs& a, cudaStream_t s);
 // The merge; always launched right after launch_cache_decode, on the same stream.
 cudaError_t launch_cache_combine(const CacheDecodeArgs& a, cudaStream_t s);
 

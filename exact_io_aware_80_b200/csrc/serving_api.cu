@@ -238,7 +238,7 @@ fa_status fa_decode_fp8(const void* q, const void* k8, const void* v8, const flo
   a.status = fa::device_status_word();
   if (!a.status) return FA_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = fa::launch_cache_decode(a, 0, s);
+  cudaError_t e = fa::launch_cache_decode(a, s);
   if (e == cudaSuccess) e = fa::launch_cache_combine(a, s);
   return from_cuda(e);
 }
@@ -313,6 +313,7 @@ fa_status fa_decode_shared_prefix(const void* q, const void* k_prefix, const voi
   a.Nk_max = Nk_max;
   a.d = d;
   a.prefix_splits = prefix_splits;
+  a.after_prefix = 1;
   a.prefix_chunk = pchunk;
   const int sms = fa::device_sm_count();
   const long long work = prefix_row_blocks(B, Hq / Hkv) * Hkv * prefix_splits;
@@ -323,7 +324,7 @@ fa_status fa_decode_shared_prefix(const void* q, const void* k_prefix, const voi
   if (!a.status) return FA_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = fa::launch_prefix_sm100(a, s);
-  if (e == cudaSuccess) e = fa::launch_cache_decode(a, 1, s);
+  if (e == cudaSuccess) e = fa::launch_cache_decode(a, s);
   if (e == cudaSuccess) e = fa::launch_cache_combine(a, s);
   return from_cuda(e);
 }
