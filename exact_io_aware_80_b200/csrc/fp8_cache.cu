@@ -17,6 +17,7 @@
 // 16-byte store of codes), so d / 16 threads hold a row and its maximum is
 // log2(d / 16) shuffles.
 #include "common.cuh"
+#include "kernels.h"
 #include "serving.h"
 
 namespace fa {
@@ -35,6 +36,16 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
+// The same of pairs of 16-bit values, which are compared as they are.
+template <typename T>
+__device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if constexpr (Elem<T>::kBf16)
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else
+    asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
 
 // Row r = (b n + i) Hkv + h of the 16-bit tensors.
 struct Rows {
@@ -49,36 +60,29 @@ __device__ __forceinline__ Row row_at(const Rows& rows, uint32_t r) {
   return Row{b, bi - b * rows.n.d, r - bi * rows.Hkv.d};
 }
 
-// E4M3 codes of 16 values x / s.  For 2^-90 <= s <= 2^90 a quotient is y = x r with r = RN(1 / s),
-// corrected once by its own remainder: q = y + (x - y s) r, which is RN(x / s) as long as nothing
-// leaves the normal range (Markstein, "Computation of elementary functions on the IBM RISC
-// System/6000 processor", 1990).  Quotients small enough to leave it have the code +-0 either way;
-// -0 alone loses its sign in the correction and takes y's.  Other scales divide.
+// E4M3 codes of 16 values x / s, given as n = -x.  FAST, for 2^-90 <= s <= 2^90: a quotient is y = x r
+// with r = RN(1 / s), corrected once by its own remainder, q = y - (y s - x) r, which is RN(x / s) as
+// long as nothing leaves the normal range (Markstein, "Computation of elementary functions on the IBM
+// RISC System/6000 processor", 1990).  Quotients small enough to leave it have the code +-0 either way,
+// and taken in this order the remainder of an exact quotient is +0, so that -0 keeps its sign.
 template <bool FAST>
-__device__ __forceinline__ uint4 codes16(const float (&x)[16], float s) {
+__device__ __forceinline__ uint4 codes16(const float2 (&n)[8], float s) {
   const float r = __frcp_rn(s);
-  uint32_t c[4];
+  uint32_t half[8];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint32_t half[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const float2 v = make_float2(x[4 * i + 2 * k], x[4 * i + 2 * k + 1]);
-      float2 q;
-      if constexpr (FAST) {
-        const float2 y = __fmul2_rn(v, make_float2(r, r));
-        const float2 rem = __ffma2_rn(y, make_float2(-s, -s), v);
-        q = __ffma2_rn(rem, make_float2(r, r), y);
-        q.x = __uint_as_float(__float_as_uint(q.x) | (__float_as_uint(y.x) & 0x80000000u));
-        q.y = __uint_as_float(__float_as_uint(q.y) | (__float_as_uint(y.y) & 0x80000000u));
-      } else {
-        q = make_float2(__fdiv_rn(v.x, s), __fdiv_rn(v.y, s));
-      }
-      half[k] = e4m3x2(q.x, q.y);
+  for (int i = 0; i < 8; ++i) {
+    float2 q;
+    if constexpr (FAST) {
+      const float2 y = __fmul2_rn(n[i], make_float2(-r, -r));
+      const float2 rem = __ffma2_rn(y, make_float2(s, s), n[i]);
+      q = __ffma2_rn(rem, make_float2(-r, -r), y);
+    } else {
+      q = make_float2(__fdiv_rn(-n[i].x, s), __fdiv_rn(-n[i].y, s));
     }
-    c[i] = half[0] | (half[1] << 16);
+    half[i] = e4m3x2(q.x, q.y);
   }
-  return make_uint4(c[0], c[1], c[2], c[3]);
+  return make_uint4(half[0] | (half[1] << 16), half[2] | (half[3] << 16), half[4] | (half[5] << 16),
+                    half[6] | (half[7] << 16));
 }
 
 // grid: (row groups, 2); y = 0 appends K rows, 1 V rows.  D / 16 consecutive threads hold a row.
@@ -112,60 +116,53 @@ __global__ void __launch_bounds__(kThreads) append_kernel(Fp8CacheArgs p, Rows r
     }
   }
   const uint32_t u[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
-  float x[16];
+  uint32_t most = u[0] & 0x7FFF7FFFu;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float2 f = Elem<T>::unpack(u[i]);
-    x[2 * i] = f.x;
-    x[2 * i + 1] = f.y;
-  }
-  float amax = 0.f;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) amax = max_nan(amax, fabsf(x[i]));
+  for (int i = 1; i < 8; ++i) most = max2_nan<T>(most, u[i] & 0x7FFF7FFFu);
+  const float2 both = Elem<T>::unpack(most);
+  float amax = max_nan(both.x, both.y);
 #pragma unroll
   for (int o = D / 32; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
   const float s = amax == 0.f ? 1.f : __fdiv_rn(amax, 448.f);
+  float2 n[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) n[i] = Elem<T>::unpack(u[i] ^ 0x80008000u);
   if (codes) {
     *reinterpret_cast<uint4*>(codes + 16 * unit) =
-        s >= 0x1p-90f && s <= 0x1p90f ? codes16<true>(x, s) : codes16<false>(x, s);
+        s >= 0x1p-90f && s <= 0x1p90f ? codes16<true>(n, s) : codes16<false>(n, s);
     if (unit == 0) *scale = s;
   }
 }
 
-// 16 E4M3 codes times s, as two 16-byte vectors of T.
+// 8 E4M3 codes times s, as a 16-byte vector of T.
 template <typename T>
-__device__ __forceinline__ void decode16(const uint4 c, float s, uint4 (&out)[2]) {
-  const uint32_t u[4] = {c.x, c.y, c.z, c.w};
-  uint32_t w[8];
+__device__ __forceinline__ uint4 decode8(const uint2 c, float s) {
+  const uint32_t u[2] = {c.x, c.y};
+  uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      uint32_t h2;
-      asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"((uint16_t)(u[i] >> (16 * k))));
-      const float2 f = Elem<__half>::unpack(h2);
-      w[2 * i + k] = Elem<T>::pack(f.x * s, f.y * s);
-    }
+    uint32_t h2;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"((uint16_t)(u[i >> 1] >> (16 * (i & 1)))));
+    const float2 f = Elem<__half>::unpack(h2);
+    w[i] = Elem<T>::pack(f.x * s, f.y * s);
   }
-  out[0] = make_uint4(w[0], w[1], w[2], w[3]);
-  out[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// grid: (row groups, 2).  Rows at or past a sequence's length come out as zeros.  A thread takes 16
-// codes of kReadRows rows, whose loads it issues together.
-constexpr int kReadRows = 2;
-template <typename T, int D>
+// grid: (row groups, 2).  Rows at or past a sequence's length come out as zeros.  A thread takes 8 codes
+// (so that a warp's 16-byte stores are one stretch) of ROWS rows, whose loads it issues together.
+template <typename T, int D, int ROWS>
 __global__ void __launch_bounds__(kThreads) read_kernel(Fp8CacheArgs p, Rows rows) {
   wait_for_earlier_grids();
-  constexpr int kUnits = D / 16, kPer = kThreads / kUnits;
+  constexpr int kUnits = D / 8, kPer = kThreads / kUnits;
   const bool isv = blockIdx.y != 0;
-  const uint32_t r0 = blockIdx.x * (kPer * kReadRows) + threadIdx.x / kUnits;
+  const uint32_t r0 = blockIdx.x * (kPer * ROWS) + threadIdx.x / kUnits;
   const int unit = threadIdx.x % kUnits;
-  uint4 c[kReadRows];
-  float s[kReadRows];
-  bool live[kReadRows];
+  uint2 c[ROWS];
+  float s[ROWS];
+  bool live[ROWS];
 #pragma unroll
-  for (int k = 0; k < kReadRows; ++k) {
+  for (int k = 0; k < ROWS; ++k) {
     const uint32_t r = r0 + k * kPer;
     live[k] = false;
     if (r < rows.count) {
@@ -176,22 +173,18 @@ __global__ void __launch_bounds__(kThreads) read_kernel(Fp8CacheArgs p, Rows row
         if (FA_IN_BOUNDS(p.status, crow, (long)p.B * p.Nk_max * p.Hkv) &&
             FA_IN_BOUNDS(p.status, srow, (long)p.B * p.Nk_max * p.Hkv)) {
           live[k] = true;
-          c[k] = reinterpret_cast<const uint4*>((isv ? p.v8 : p.k8) + crow * D)[unit];
+          c[k] = reinterpret_cast<const uint2*>((isv ? p.v8 : p.k8) + crow * D)[unit];
           s[k] = (isv ? p.v_scale : p.k_scale)[srow];
         }
       }
     }
   }
 #pragma unroll
-  for (int k = 0; k < kReadRows; ++k) {
+  for (int k = 0; k < ROWS; ++k) {
     const uint32_t r = r0 + k * kPer;
-    if (r < rows.count && FA_IN_BOUNDS(p.status, r, rows.count)) {
-      uint4 w[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-      if (live[k]) decode16<T>(c[k], s[k], w);
-      uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(isv ? p.v_out : p.k_out) + (long)r * D) + 2 * unit;
-      dst[0] = w[0];
-      dst[1] = w[1];
-    }
+    if (r < rows.count && FA_IN_BOUNDS(p.status, r, rows.count))
+      reinterpret_cast<uint4*>(static_cast<uint16_t*>(isv ? p.v_out : p.k_out) + (long)r * D)[unit] =
+          live[k] ? decode8<T>(c[k], s[k]) : make_uint4(0u, 0u, 0u, 0u);
   }
 }
 
@@ -203,11 +196,18 @@ cudaError_t launch_append(const Fp8CacheArgs& a, cudaStream_t s) {
   const uint32_t per = kThreads / (D / 16);
   return launch_dependent(append_kernel<T, D>, dim3((rows.count + per - 1) / per, 2), kThreads, 0, s, a, rows);
 }
+template <typename T, int D, int ROWS>
+cudaError_t launch_read_rows(const Fp8CacheArgs& a, const Rows& rows, cudaStream_t s) {
+  const uint32_t per = kThreads / (D / 8) * ROWS;
+  return launch_dependent(read_kernel<T, D, ROWS>, dim3((rows.count + per - 1) / per, 2), kThreads, 0, s, a, rows);
+}
 template <typename T, int D>
 cudaError_t launch_read(const Fp8CacheArgs& a, cudaStream_t s) {
   const Rows rows = rows_of(a);
-  const uint32_t per = kThreads / (D / 16) * kReadRows;
-  return launch_dependent(read_kernel<T, D>, dim3((rows.count + per - 1) / per, 2), kThreads, 0, s, a, rows);
+  // 134 MB of codes: 61.9 us with four rows a thread, 81.5, 66.4 and 67.2 with one, two and eight; one where
+  // four would leave SMs idle
+  const bool few = (long)rows.count * (D / 8) < 4l * kThreads * device_sm_count();
+  return few ? launch_read_rows<T, D, 1>(a, rows, s) : launch_read_rows<T, D, 4>(a, rows, s);
 }
 
 }  // namespace

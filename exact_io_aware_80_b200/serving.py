@@ -42,10 +42,9 @@ def _dt(t):
 
 
 def _device(t):
-    dev = t.device
-    if dev.type != "cuda":
+    if not t.is_cuda:
         raise ValueError("libfa.so takes CUDA tensors only (no CPU path)")
-    return dev
+    return t.device
 
 
 def _check(name, t, dtype, shape, dev, contiguous=True):
@@ -60,12 +59,17 @@ def _check(name, t, dtype, shape, dev, contiguous=True):
     raise ValueError(f"{name} must be contiguous")
 
 
+_entries: dict = {}
+
+
 def _call(dev, name, *args):
     """The C entry point with ``dev`` current, on its current stream."""
+    fn = _entries.get(name)
+    if fn is None:
+        fn = _entries[name] = getattr(_lib.load(), name)
     torch = _torch()
-    fn = getattr(_lib.load(), name)
     index = dev.index
-    if index == torch.cuda.current_device():
+    if index == torch._C._cuda_getDevice():
         rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(dev):
@@ -74,11 +78,10 @@ def _call(dev, name, *args):
         raise _lib.FAError(name, rc)
 
 
-def _strides(name, t):
+def _strides(name, t, B, N, H, d):
     """(batch, token) strides of [B, N, H, d] whose heads are contiguous."""
-    B, N, H, d = t.shape
     sb, sn, sh, sd = t.stride()
-    if (sd != 1 and d > 1) or (sh != d and H > 1):
+    if (sh != d and H > 1) or (sd != 1 and d > 1):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
     return (sb if B > 1 else 0), (sn if N > 1 else 0)
 
@@ -140,7 +143,7 @@ def _rotary(q, k, positions, table, interleaved, magnitude, inverse, q_out, k_ou
     _check("positions", positions, torch.int32, (B, N) if each else (N,), dev)
     pairs = table.numel()
     _check("table", table, torch.int64, (pairs,), dev)
-    q_st, k_st, Hkv, kp, kop = _strides("q", q), (0, 0), 0, 0, 0
+    (q_bs, q_ts), k_bs, k_ts, Hkv, kp, kop = _strides("q", q, B, N, Hq, d), 0, 0, 0, 0, 0
     if q_out is None:
         q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
     else:
@@ -149,14 +152,15 @@ def _rotary(q, k, positions, table, interleaved, magnitude, inverse, q_out, k_ou
         Hkv = k.shape[2]
         shape = (B, N, Hkv, d)
         _check("k", k, dtype, shape, dev, contiguous=False)
-        k_st = _strides("k", k)
+        k_bs, k_ts = _strides("k", k, B, N, Hkv, d)
         if k_out is None:
             k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
         else:
             _check("k_out", k_out, dtype, shape, dev)
         kp, kop = k.data_ptr(), k_out.data_ptr()
     _call(dev, "fa_rotary", q.data_ptr(), kp, q_out.data_ptr(), kop, positions.data_ptr(), table.data_ptr(), B, N,
-          Hq, Hkv, d, 2 * pairs, int(interleaved), int(inverse), magnitude, *q_st, *k_st, N if each else 0, dt)
+          Hq, Hkv, d, 2 * pairs, int(interleaved), int(inverse), magnitude, q_bs, q_ts, k_bs, k_ts,
+          N if each else 0, dt)
     return q_out, k_out
 
 
@@ -208,7 +212,7 @@ def fp8_cache_append(k, v, k8, v8, k_scale, v_scale, start, counts=None):
         _check("counts", counts, torch.int32, (B,), dev)
     _call(dev, "fa_fp8_cache_append", k.data_ptr(), v.data_ptr(), k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(),
           v_scale.data_ptr(), start.data_ptr(), 0 if counts is None else counts.data_ptr(), B, n, Hkv, Nk_max, d,
-          *_strides("k", k), *_strides("v", v), dt)
+          *_strides("k", k, B, n, Hkv, d), *_strides("v", v, B, n, Hkv, d), dt)
 
 
 def fp8_cache_read(k8, v8, k_scale, v_scale, seqlens_k, Nk: int | None = None, dtype=None):

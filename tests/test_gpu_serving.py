@@ -167,7 +167,7 @@ APPEND = [
 def test_append_and_read(fa, B, n, H, d, Nk, dt, start, counts):
     k, v = normal((B, n, H, d), DT[dt], 21), normal((B, n, H, d), DT[dt], 22, size=300.0)
     k[:, 0, 0] = 0  # a row of zeros
-    v[0, 0, 0, 1:] = 0  # a single value
+    v[0, 0, 0, 1:] = -0.0  # a single value among negative zeros, whose sign a code keeps
     k[-1, -1, -1] *= 1e-6  # fp16: values below its normal range
     cache = empty_cache(B, Nk, H, d)
     want = [c.cpu().numpy().copy() for c in cache]
