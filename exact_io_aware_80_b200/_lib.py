@@ -61,7 +61,7 @@ SIGNATURES = {
     "fa_rotary": (_I, [_P] * 6 + [_I] * 8 + [_F] + [_L] * 5 + [_I, _P]),
     "fa_fp8_cache_append": (_I, [_P] * 8 + [_I] * 5 + [_L] * 4 + [_I, _P]),
     "fa_fp8_cache_read": (_I, [_P] * 7 + [_I] * 5 + [_I, _P]),
-    "fa_decode_fp8_workspace_bytes": (ctypes.c_size_t, [_I] * 5),
+    "fa_decode_fp8_workspace_bytes": (ctypes.c_size_t, [_I] * 6),
     "fa_decode_fp8": (_I, [_P] * 9 + [_I] * 5 + [_F, _I, _P]),
     "fa_decode_prefix_splits": (_I, [_I] * 8),
     "fa_decode_shared_prefix": (_I, [_P] * 11 + [_I] * 6 + [_F, _I, _I, _P]),
@@ -244,8 +244,8 @@ def fa_fp8_cache_read(k8, v8, k_scale, v_scale, seqlens_k, k, v, B, Nk, Hkv, Nk_
                                                                 Nk_max, d, dt, stream))
 
 
-def fa_decode_fp8_workspace_bytes(B, Hq, Hkv, prefix_splits, d):
-    return load().fa_decode_fp8_workspace_bytes(B, Hq, Hkv, prefix_splits, d)
+def fa_decode_fp8_workspace_bytes(B, Hq, Hkv, Nk_max, prefix_splits, d):
+    return load().fa_decode_fp8_workspace_bytes(B, Hq, Hkv, Nk_max, prefix_splits, d)
 
 
 def fa_decode_fp8(q, k8, v8, k_scale, v_scale, seqlens_k, o, lse, workspace, B, Hq, Hkv, Nk_max, d, scale, dt, stream):

@@ -19,6 +19,11 @@
 // read the same tokens' rows together (a line through the heads as well, whose CTAs
 // stand at different tokens, lost 13 % of the bandwidth).
 //
+// Small batches (SOLO): a cluster of up to 8 CTAs per sequence and KV head shares
+// that sequence's blocks out and merges through distributed shared memory, with the
+// few partials of a shared prefix if there is one: one launch instead of two, and
+// no workspace of its own.
+//
 // A CTA.  The group's Hq / Hkv query rows share every byte it reads.  Each of the
 // four warps streams its own kStep keys of a block through its own two cp.async
 // buffers (no block barrier until a sequence's end) with its own running (m, l, O);
@@ -85,6 +90,8 @@ template <int D, bool F8, int NB>
 struct Smem {
   static constexpr int kOffM = 4 * 2 * Ring<D, F8>::kStage;  // m, l [4][8 NB] fp32, then the offset of each warp's O
   static constexpr int kBytes = kOffM + 4 * 8 * NB * 2 * 4 + 4 * 4;
+  static constexpr int kOffSolo = (kBytes + 15) / 16 * 16;  // SOLO: this CTA's O [8 NB][D] and LSE [8 NB]
+  static constexpr int kSoloBytes = kOffSolo + 8 * NB * (D + 1) * 4;
   static_assert(8 * NB * D * 4 <= Ring<D, F8>::kStage, "a warp's O is merged through its free buffer");
 };
 
@@ -133,7 +140,30 @@ struct Item {
   int blk, blks;     // that block within the sequence, and the sequence's blocks
 };
 
-template <typename T, int D, bool F8, int NB, bool REST>
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+// Shared memory of the cluster's CTA `rank` at this CTA's address `addr`.
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float cluster_load(uint32_t addr) {
+  float x;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(addr) : "memory");
+  return x;
+}
+__device__ __forceinline__ float4 cluster_load4(uint32_t addr) {
+  float4 x;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+               : "r"(addr)
+               : "memory");
+  return x;
+}
+
+template <typename T, int D, bool F8, int NB, bool REST, bool SOLO>
 __global__ void __launch_bounds__(kThreads, cache_ctas_per_sm(D, F8, NB == 2)) cache_decode_kernel(CacheDecodeArgs p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   using R = Ring<D, F8>;
@@ -142,11 +172,18 @@ __global__ void __launch_bounds__(kThreads, cache_ctas_per_sm(D, F8, NB == 2)) c
   constexpr int MB = R::kBlocks;
   constexpr int kBlock = 4 * R::kStep;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int G = p.Hq / p.Hkv, hk = blockIdx.x % p.Hkv, cta = blockIdx.x / p.Hkv;
+  const int G = p.Hq / p.Hkv;
+  int rank = 0, ranks = 1;  // SOLO: place in the cluster
+  if constexpr (SOLO) {
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    ranks = p.solo;
+  }
+  const int unit = SOLO ? blockIdx.x / ranks : blockIdx.x;
+  const int hk = unit % p.Hkv, cta = unit / p.Hkv;  // SOLO: cta is the sequence
   // behind every earlier grid but a prefix kernel's, which itself started behind all others; the merge,
   // launched next, may become resident
   if (!p.after_prefix) asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if constexpr (!SOLO) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   const uint32_t ring = smem_u32(smem) + warp * 2 * R::kStage;
   const uint8_t* const ring_g = smem + warp * 2 * R::kStage;
@@ -159,9 +196,15 @@ __global__ void __launch_bounds__(kThreads, cache_ctas_per_sm(D, F8, NB == 2)) c
 // itself: a lane sums the blocks of a stretch of sequences, and the one whose stretch holds begin walks it
   auto length = [&](int b) { return min(max(p.seqlens[b], 0), p.Nk_max); };
   auto blocks = [&](int n) { return (n + kBlock - 1) / kBlock; };
-  int begin, end, W, C;  // W < 2^31: a block of a head takes 4 KB at least
+  int begin, end, W = 0, C = 0;  // W < 2^31: a block of a head takes 4 KB at least
   int cb = 0, cblk = 0, cn = 0, cpos;  // the cursor: block cblk of sequence cb, of cn keys, at place cpos
-  {
+  if constexpr (SOLO) {
+    cb = cta;
+    cn = length(cb);
+    const int nb = blocks(cn);
+    cpos = cblk = begin = (int)((long long)rank * nb / ranks);
+    end = (int)((long long)(rank + 1) * nb / ranks);
+  } else {
     const int per = (p.B + 31) / 32;
     const int b0 = min(lane * per, p.B), b1 = min(b0 + per, p.B);
     int mine = 0;
@@ -296,8 +339,11 @@ __global__ void __launch_bounds__(kThreads, cache_ctas_per_sm(D, F8, NB == 2)) c
     }
   };
 
+  float* const solo_o = reinterpret_cast<float*>(smem + L::kOffSolo);
+  float* const solo_lse = solo_o + 8 * NB * D;
   Item cur;
   bool have = next(cur);
+  if (SOLO && !have && tid < G) solo_lse[tid] = -INFINITY;
   int c0 = 0;  // buffer of the current item's first block
   if (have) {
     aim(cur);
@@ -550,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, cache_ctas_per_sm(D, F8, NB == 2)) c
     const long slots = (long)p.Hkv * (p.B + gridDim.x / p.Hkv);
     const long slot = (long)hk * (p.B + gridDim.x / p.Hkv) + cur.b + cta;
     // whoever has a sequence's first block knows which CTAs have the others
-    if (tid == 0 && cur.blk == 0 && hk == 0 && FA_IN_BOUNDS(p.status, cur.b, p.B))
+    if (!SOLO && tid == 0 && cur.blk == 0 && hk == 0 && FA_IN_BOUNDS(p.status, cur.b, p.B))
       p.spans[cur.b] = make_int2(cta, (int)(((long long)(cur.pos + cur.blks) * C - 1) / W));
     for (int idx = 4 * tid; idx < G * D; idx += 4 * kThreads) {
       const int g = idx / D;
@@ -571,11 +617,15 @@ __global__ void __launch_bounds__(kThreads, cache_ctas_per_sm(D, F8, NB == 2)) c
         o.z += x.z * f;
         o.w += x.w * f;
       }
-      if (FA_IN_BOUNDS(p.status, slot, slots)) {
-        const float inv = lt == 0.f ? 0.f : 1.f / lt;
-        *reinterpret_cast<float4*>(p.o_cache + slot * G * D + idx) =
-            lt == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-        if (idx % D == 0) p.lse_cache[slot * G + g] = (mu - (mx == -INFINITY ? 0.f : kLift) + log2f(lt)) * kLn2;
+      const float inv = lt == 0.f ? 0.f : 1.f / lt;
+      const float4 part = lt == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+      const float lse = (mu - (mx == -INFINITY ? 0.f : kLift) + log2f(lt)) * kLn2;
+      if constexpr (SOLO) {
+        *reinterpret_cast<float4*>(solo_o + idx) = part;
+        if (idx % D == 0) solo_lse[g] = lse;
+      } else if (FA_IN_BOUNDS(p.status, slot, slots)) {
+        *reinterpret_cast<float4*>(p.o_cache + slot * G * D + idx) = part;
+        if (idx % D == 0) p.lse_cache[slot * G + g] = lse;
       }
     }
     __syncthreads();  // the free buffers may be loaded into again
@@ -583,6 +633,45 @@ __global__ void __launch_bounds__(kThreads, cache_ctas_per_sm(D, F8, NB == 2)) c
     have = more;
   }
   cp_async_wait<0>();
+  if constexpr (SOLO) {
+    if (p.after_prefix) asm volatile("griddepcontrol.wait;" ::: "memory");
+    cluster_sync();
+    const uint32_t so = smem_u32(solo_o), sl = smem_u32(solo_lse);
+    for (int idx = 4 * (rank * kThreads + tid); idx < G * D; idx += 4 * kThreads * ranks) {
+      const int g = idx / D, col = idx - g * D;
+      const long row = (long)cta * p.Hq + (long)hk * G + g;
+      if (!FA_IN_BOUNDS(p.status, row, (long)p.B * p.Hq)) continue;
+      const float* const plse = p.lse_part + row * p.prefix_splits;
+      const float* const po = p.o_part + row * p.prefix_splits * D + col;
+      float mx = -INFINITY;
+      for (int r = 0; r < ranks; ++r) mx = fmaxf(mx, cluster_load(cluster_addr(sl + 4 * g, r)));
+      for (int i = 0; i < p.prefix_splits; ++i) mx = fmaxf(mx, plse[i]);
+      const float mu = mx == -INFINITY ? 0.f : mx;
+      float l = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      auto add = [&](float lse, float4 x) {
+        const float w = ex2((lse - mu) * kLog2e);
+        l += w;
+        o.x += w * x.x;
+        o.y += w * x.y;
+        o.z += w * x.z;
+        o.w += w * x.w;
+      };
+      for (int r = 0; r < ranks; ++r) {
+        const float lse = cluster_load(cluster_addr(sl + 4 * g, r));
+        if (lse != -INFINITY) add(lse, cluster_load4(cluster_addr(so + 4 * idx, r)));  // else nothing was left there
+      }
+#pragma unroll 4
+      for (int i = 0; i < p.prefix_splits; ++i) add(plse[i], *reinterpret_cast<const float4*>(po + (long)i * D));
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      if (l == 0.f) o = make_float4(0.f, 0.f, 0.f, 0.f);  // no key: O = 0, LSE = -inf
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + row * D + col) =
+          make_uint2(Elem<T>::pack(o.x * inv, o.y * inv), Elem<T>::pack(o.z * inv, o.w * inv));
+      if (col == 0) p.lse[row] = mu + logf(l);
+    }
+    cluster_sync();  // no CTA leaves while another may read its shared memory
+    return;
+  }
   // after a prefix kernel this grid must not end before that one has, since the merge waits only for
   // this one
   if (blockIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -668,11 +757,17 @@ __global__ void __launch_bounds__(combine_threads(WARPS)) cache_combine_kernel(C
 
 template <typename T, int D, bool F8, int NB, bool REST>
 cudaError_t launch_part(const CacheDecodeArgs& a, cudaStream_t s) {
-  auto kern = cache_decode_kernel<T, D, F8, NB, REST>;
-  constexpr int smem = Smem<D, F8, NB>::kBytes;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  using L = Smem<D, F8, NB>;
+  if (a.solo > 0) {
+    auto kern = cache_decode_kernel<T, D, F8, NB, REST, true>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSoloBytes);
+    if (e != cudaSuccess) return e;
+    return launch_dependent_clusters(kern, dim3(a.B * a.Hkv * a.solo), a.solo, kThreads, L::kSoloBytes, s, a);
+  }
+  auto kern = cache_decode_kernel<T, D, F8, NB, REST, false>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
   if (e != cudaSuccess) return e;
-  return launch_dependent(kern, dim3(a.cache_ctas), kThreads, smem, s, a);
+  return launch_dependent(kern, dim3(a.cache_ctas), kThreads, L::kBytes, s, a);
 }
 
 template <typename T, int D, bool F8, bool REST>

@@ -38,18 +38,27 @@ struct FastDiv {
 // resident before that has finished, and orders itself behind it (and behind all before it) with
 // griddepcontrol.wait ahead of its first access to global memory.
 template <typename... Params, typename... Args>
-cudaError_t launch_dependent(void (*kern)(Params...), dim3 grid, int threads, int smem, cudaStream_t s, Args&&... args) {
+cudaError_t launch_dependent_clusters(void (*kern)(Params...), dim3 grid, int cluster, int threads, int smem,
+                                      cudaStream_t s, Args&&... args) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cudaLaunchAttribute attr[2]{};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 0 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
+}
+template <typename... Params, typename... Args>
+cudaError_t launch_dependent(void (*kern)(Params...), dim3 grid, int threads, int smem, cudaStream_t s, Args&&... args) {
+  return launch_dependent_clusters(kern, grid, 0, threads, smem, s, std::forward<Args>(args)...);
 }
 #ifdef __CUDACC__
 // Behind every earlier grid, and then: the next one may become resident.
@@ -116,6 +125,7 @@ struct CacheDecodeArgs {
   int B, Hq, Hkv, Np, Nk_max, d;
   int prefix_splits, prefix_chunk;  // keys per prefix split, a multiple of 128
   int after_prefix;                 // the launch before the cache kernel's is the prefix kernel's
+  int solo;                         // > 0: CTAs of a cluster per sequence and KV head, which merge alone
   int cache_ctas;                   // a multiple of Hkv, at most max(kMaxCacheCtas, Hkv)
   float scale;
   int bf16;

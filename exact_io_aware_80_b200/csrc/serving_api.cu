@@ -49,6 +49,17 @@ fa_status check_decode(int B, int Hq, int Hkv, int Nk_max, int d, float scale, f
   return FA_OK;
 }
 
+// CTAs of a cluster per sequence and KV head for a batch small enough to go without a separate merge
+// (0: too large): as many as 128 keys each leave, all resident at once (3 an SM), at most 1024 keys
+// each and 8 of a prefix's partials a row.
+int solo_of(int B, int Hkv, int Nk_max, int prefix_splits) {
+  const long long units = (long long)B * Hkv, most = 3 * 148;
+  if (units > most || prefix_splits > 8) return 0;
+  int n = 8;
+  while (n > 1 && (units * n > most || 128ll * (n / 2) >= Nk_max)) n /= 2;
+  return Nk_max <= 1024 * n ? n : 0;
+}
+
 // Bytes of the partials, and where each kind lies: O of the prefix and of the caches, then the LSEs, then the spans.
 struct Workspace {
   size_t o_cache, lse_part, lse_cache, spans, bytes;
@@ -203,17 +214,20 @@ fa_status fa_fp8_cache_read(const void* k8, const void* v8, const float* k_scale
   return from_cuda(fa::launch_fp8_cache_read(a, static_cast<cudaStream_t>(stream)));
 }
 
-size_t fa_decode_fp8_workspace_bytes(int B, int Hq, int Hkv, int prefix_splits, int d) {
-  if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || prefix_splits < 0 || d < 1) return 0;
+size_t fa_decode_fp8_workspace_bytes(int B, int Hq, int Hkv, int Nk_max, int prefix_splits, int d) {
+  if (B < 1 || Hq < 1 || Hkv < 1 || Nk_max < 1 || Hq % Hkv != 0 || prefix_splits < 0 || d < 1) return 0;
+  if (prefix_splits == 0 && solo_of(B, Hkv, Nk_max, 0) > 0) return 0;
   return workspace_of(B, Hq, Hkv, prefix_splits, d).bytes;
 }
 
 fa_status fa_decode_fp8(const void* q, const void* k8, const void* v8, const float* k_scale, const float* v_scale,
                         const int* seqlens_k, void* o, float* lse, void* workspace, int B, int Hq, int Hkv, int Nk_max,
                         int d, float scale, fa_dtype dt, fa_stream_t stream) {
-  if (!q || !k8 || !v8 || !k_scale || !v_scale || !seqlens_k || !o || !lse || !workspace) return FA_ERR_INVALID;
+  if (!q || !k8 || !v8 || !k_scale || !v_scale || !seqlens_k || !o || !lse) return FA_ERR_INVALID;
   const fa_status st = check_decode(B, Hq, Hkv, Nk_max, d, scale, dt);
   if (st != FA_OK) return st;
+  const int solo = solo_of(B, Hkv, Nk_max, 0);
+  if (!workspace && !solo) return FA_ERR_INVALID;
   if (!aligned(q, 16) || !aligned(k8, 16) || !aligned(v8, 16) || !aligned(o, 16) || !aligned(workspace, 16) ||
       !aligned(k_scale, 4) || !aligned(v_scale, 4) || !aligned(seqlens_k, 4) || !aligned(lse, 4))
     return FA_ERR_ALIGN;
@@ -232,6 +246,7 @@ fa_status fa_decode_fp8(const void* q, const void* k8, const void* v8, const flo
   a.Hkv = Hkv;
   a.Nk_max = Nk_max;
   a.d = d;
+  a.solo = solo;
   a.cache_ctas = cache_ctas_of(B, Hkv, Nk_max, d, Hq / Hkv, true, fa::device_sm_count(), 0);
   a.scale = scale;
   a.bf16 = dt == FA_BF16 ? 1 : 0;
@@ -239,7 +254,7 @@ fa_status fa_decode_fp8(const void* q, const void* k8, const void* v8, const flo
   if (!a.status) return FA_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = fa::launch_cache_decode(a, s);
-  if (e == cudaSuccess) e = fa::launch_cache_combine(a, s);
+  if (e == cudaSuccess && !a.solo) e = fa::launch_cache_combine(a, s);
   return from_cuda(e);
 }
 
@@ -315,6 +330,7 @@ fa_status fa_decode_shared_prefix(const void* q, const void* k_prefix, const voi
   a.prefix_splits = prefix_splits;
   a.after_prefix = 1;
   a.prefix_chunk = pchunk;
+  a.solo = solo_of(B, Hkv, Nk_max, prefix_splits);
   const int sms = fa::device_sm_count();
   const long long work = prefix_row_blocks(B, Hq / Hkv) * Hkv * prefix_splits;
   a.cache_ctas = cache_ctas_of(B, Hkv, Nk_max, d, Hq / Hkv, k_scale != nullptr, sms, std::min<long long>(work, sms));
@@ -325,7 +341,7 @@ fa_status fa_decode_shared_prefix(const void* q, const void* k_prefix, const voi
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = fa::launch_prefix_sm100(a, s);
   if (e == cudaSuccess) e = fa::launch_cache_decode(a, s);
-  if (e == cudaSuccess) e = fa::launch_cache_combine(a, s);
+  if (e == cudaSuccess && !a.solo) e = fa::launch_cache_combine(a, s);
   return from_cuda(e);
 }
 

@@ -240,7 +240,7 @@ def _plan(device, B, Hq, Hkv, Np, Nk_max, d, fp8, prefix_splits):
     if prefix_splits is None:
         with _torch().cuda.device(device):
             prefix_splits = _lib.fa_decode_prefix_splits(B, Hq, Hkv, Np, Nk_max, d, fp8)
-    return prefix_splits, _lib.fa_decode_fp8_workspace_bytes(B, Hq, Hkv, prefix_splits, d)
+    return prefix_splits, _lib.fa_decode_fp8_workspace_bytes(B, Hq, Hkv, Nk_max, prefix_splits, d)
 
 
 def _decode_buffers(q, seqlens_k, need, workspace, out, lse):
@@ -251,7 +251,7 @@ def _decode_buffers(q, seqlens_k, need, workspace, out, lse):
     _check("q", q, dtype, shape, dev)
     _check("seqlens_k", seqlens_k, torch.int32, (B,), dev)
     if workspace is None:
-        workspace = q.new_empty(need, dtype=torch.uint8)
+        workspace = q.new_empty(need, dtype=torch.uint8) if need else None
     elif workspace.device != dev or not workspace.is_contiguous() or \
             workspace.numel() * workspace.element_size() < need:
         raise ValueError(f"workspace must be contiguous, on the device of q and hold {need} bytes")
@@ -277,7 +277,8 @@ def decode_fp8(q, k8, v8, k_scale, v_scale, seqlens_k, scale: float | None = Non
     _, need = _plan(dev.index, B, Hq, Hkv, 0, Nk_max, d, True, 0)
     workspace, out, lse = _decode_buffers(q, seqlens_k, need, workspace, out, lse)
     _call(dev, "fa_decode_fp8", q.data_ptr(), k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-          seqlens_k.data_ptr(), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), B, Hq, Hkv, Nk_max, d, scale, dt)
+          seqlens_k.data_ptr(), out.data_ptr(), lse.data_ptr(), workspace.data_ptr() if need else 0, B, Hq,
+          Hkv, Nk_max, d, scale, dt)
     return out, lse
 
 

@@ -416,9 +416,11 @@ fa_status fa_fp8_cache_read(const void* k8, const void* v8, const float* k_scale
 /*
  * Workspace bytes of fa_decode_fp8 (prefix_splits = 0) and fa_decode_shared_prefix:
  * fp32 partials of B * Hq * prefix_splits rows and of at most B * Hkv + max(Hkv,
- * 1024) pieces of the caches, Hq / Hkv rows each (0 on bad sizes).
+ * 1024) pieces of the caches, Hq / Hkv rows each (0 on bad sizes).  0 also for a
+ * small batch without a prefix, which needs none; its workspace may be NULL.
+ * Calls that may overlap on the device need workspaces of their own.
  */
-size_t fa_decode_fp8_workspace_bytes(int B, int Hq, int Hkv, int prefix_splits, int d);
+size_t fa_decode_fp8_workspace_bytes(int B, int Hq, int Hkv, int Nk_max, int prefix_splits, int d);
 
 /*
  * One-token attention over an E4M3 cache (fa_fp8_cache_append): q [B,1,Hq,d] and
@@ -426,7 +428,7 @@ size_t fa_decode_fp8_workspace_bytes(int B, int Hq, int Hkv, int prefix_splits, 
  * seqlens_k[b] rows (DEVICE int32 [B], clamped into [0, Nk_max]); a sequence of
  * length 0 gets O = 0 and LSE = -inf.  The keys that the lengths leave are shared
  * out evenly among the CTAs and the pieces merged by log-sum-exp; workspace of
- * fa_decode_fp8_workspace_bytes(B, Hq, Hkv, 0, d) bytes, 16-byte aligned.
+ * fa_decode_fp8_workspace_bytes(B, Hq, Hkv, Nk_max, 0, d) bytes, 16-byte aligned.
  * scale >= 0, finite; at most 16 query heads per KV head.  Scales in the cache
  * are positive.
  */
@@ -448,7 +450,7 @@ int fa_decode_prefix_splits(int B, int Hq, int Hkv, int Np, int Nk_max, int d, i
  * or E4M3 codes with scales [B,Hkv,Nk_max].  q, o, lse, seqlens_k and limits as
  * fa_decode_fp8.  The prefix is cut into prefix_splits ranges of whole 128-key
  * tiles, none of them empty; workspace of
- * fa_decode_fp8_workspace_bytes(B, Hq, Hkv, prefix_splits, d) bytes.
+ * fa_decode_fp8_workspace_bytes(B, Hq, Hkv, Nk_max, prefix_splits, d) bytes.
  */
 fa_status fa_decode_shared_prefix(const void* q, const void* k_prefix, const void* v_prefix, const void* k_cache,
                                   const void* v_cache, const float* k_scale, const float* v_scale,

@@ -271,6 +271,11 @@ DECODE = [
     (300, 2, 2, 40, 64, "bf16", [b % 41 for b in range(300)]),  # many sequences to a CTA, more than threads
     (140, 3, 3, 300, 128, "fp16", [(61 * b) % 301 if b % 3 else 0 for b in range(140)]),
     (3, 5, 5, 70, 64, "bf16", [0, 0, 0]),
+    # too many keys or sequences for one cluster each
+    (1, 16, 1, 9000, 128, "fp16", [8500]),
+    (2, 6, 3, 5000, 128, "bf16", [4999, 17]),
+    (3, 4, 2, 8200, 64, "bf16", [0, 8200, 130]),
+    (90, 10, 5, 140, 64, "fp16", [(37 * b) % 141 for b in range(90)]),
 ]
 
 
@@ -343,6 +348,9 @@ PREFIX = [
     (65, 8, 2, 640, 20, 128, "bf16", False, 5),          # 260 rows: a second row block
     (53, 5, 1, 400, 33, 64, "fp16", True, None),      # G = 5: 25 sequences a tile
     (150, 1, 1, 257, 5, 128, "bf16", False, None),    # G = 1
+    (120, 8, 4, 600, 130, 64, "fp16", True, 3),       # the caches merged apart
+    (60, 8, 8, 200, 30, 128, "bf16", False, None),
+    (2, 8, 2, 1500, 30, 64, "bf16", True, 12),        # many prefix splits
     (40, 14, 2, 260, 9, 64, "bf16", False, 1),        # G = 7: 18 sequences a tile, 126 rows
 ]
 
@@ -439,7 +447,8 @@ def test_decode_refusals(fa):
     with pytest.raises(TypeError):
         fa.decode_fp8(q, *cache, lens.long())
     with pytest.raises(ValueError):
-        fa.decode_fp8(q, *cache, lens, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+        fa.decode_shared_prefix(q, kp, kp, cache[0], cache[1], lens, cache[2], cache[3],
+                                workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
     with pytest.raises(ValueError):
         fa.decode_fp8(q, cache[0], cache[1], cache[2].transpose(1, 2), cache[3], lens)
     with pytest.raises(ValueError):
@@ -534,7 +543,7 @@ def test_graphs_that_share_a_workspace_and_other_streams(fa):
     kp, vp = (normal((1, 333, Hkv, d), torch.bfloat16, 104 + i).cuda() for i in range(2))
     sl = ints(lens)
     P = fa.fa_decode_prefix_splits(B, Hq, Hkv, 333, N, d, True)
-    ws = torch.empty(fa.fa_decode_fp8_workspace_bytes(B, Hq, Hkv, P, d), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(fa.fa_decode_fp8_workspace_bytes(B, Hq, Hkv, N, P, d), dtype=torch.uint8, device="cuda")
 
     def a():
         return fa.decode_fp8(q[0], *cache, sl, workspace=ws)

@@ -68,7 +68,7 @@ def test_cache_read_rejects_bad_arguments(lib):
 
 def test_decode_fp8_rejects_bad_arguments(lib):
     # q, k8, v8, ks, vs, seqlens, o, lse, ws, B, Hq, Hkv, Nk_max, d, scale, dt, stream
-    base = [FAKE] * 9 + [2, 32, 8, 1024, 128, 0.1, 1, None]
+    base = [FAKE] * 9 + [200, 32, 8, 1024, 128, 0.1, 1, None]
     _rejects(lib.fa_decode_fp8, base, [
         ({0: 0}, -1), ({3: 0}, -1), ({8: 0}, -1), ({10: 33}, -1), ({9: 0}, -1), ({12: 0}, -1),
         ({14: -0.1}, -1), ({14: math.inf}, -1), ({14: math.nan}, -1),
@@ -98,9 +98,10 @@ def test_split_plans_are_accepted_shapes(lib):
                 chunk = -(-(-(-N // s)) // 128) * 128
                 assert 1 <= s <= -(-N // 128) and (s - 1) * chunk < N
     ws = _lib.fa_decode_fp8_workspace_bytes
-    assert ws(2, 8, 2, 0, 128) >= (2 * 2 + 1024) * 4 * 129 * 4 + 2 * 8
-    assert ws(2, 8, 2, 3, 64) - ws(2, 8, 2, 0, 64) >= 2 * 8 * 3 * 65 * 4
-    assert ws(2, 8, 3, 0, 64) == 0 and ws(0, 8, 2, 0, 64) == 0 and ws(2, 8, 2, -1, 64) == 0
+    assert ws(2, 8, 2, 10000, 0, 128) >= (2 * 2 + 1024) * 4 * 129 * 4 + 2 * 8
+    assert ws(2, 8, 2, 10000, 3, 64) - ws(2, 8, 2, 10000, 0, 64) >= 2 * 8 * 3 * 65 * 4
+    assert ws(2, 8, 2, 1000, 0, 128) == 0 and ws(2, 8, 2, 1000, 1, 128) > 0  # a small batch alone needs none
+    assert ws(2, 8, 3, 10000, 0, 64) == 0 and ws(0, 8, 2, 10000, 0, 64) == 0 and ws(2, 8, 2, 10000, -1, 64) == 0
 
 
 # ---------------------------------------------------------------------------
