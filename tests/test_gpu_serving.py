@@ -573,6 +573,113 @@ def test_graphs_that_share_a_workspace_and_other_streams(fa):
             assert torch.equal(x, y) and torch.equal(x, z)
 
 
+def test_calls_follow_earlier_and_precede_later_work(fa):
+    """A chain of calls over the same buffers, each input produced just before by other kernels and each
+    output read just after, with nothing waited for in between, equals the same chain with a wait after
+    every step, bit for bit (the kernels start as programmatic dependents)."""
+    B, Hq, Hkv, N, d = 24, 8, 2, 300, 64
+    table = fa.rotary_table(d)
+    kp, vp = (normal((1, 700, Hkv, d), torch.float16, 121 + i).cuda() for i in range(2))
+    big = normal((2048, 2048), torch.float16, 123).cuda()
+    src = [normal((B, 1, Hq + 2 * Hkv, d), torch.float16, 124 + i).cuda() for i in range(12)]
+    long_lens = ints([150 + b for b in range(B)])
+
+    def chain(wait):
+        cache = empty_cache(B, N, Hkv, d)
+        for c in cache[2:]:
+            c.fill_(0.01)
+        for c in cache[:2]:
+            c.fill_(0x38)
+        lens, outs = torch.zeros(B, dtype=torch.int32, device="cuda"), []
+        x, q = torch.empty_like(src[0]), torch.empty(B, 1, Hq, d, dtype=torch.float16, device="cuda")
+        for i, s in enumerate(src):
+            y = big
+            for _ in range(3):
+                y = (y @ big) * 0.01
+            x.copy_(s + 0 * y[0, 0])
+            qp, k, v = x.split([Hq, Hkv, Hkv], dim=2)
+            pos = (lens + 700).view(B, 1)
+            _, kr = fa.rotary_fwd(qp, k, pos, table, q_out=q)
+            fa.fp8_cache_append(kr, v, *cache, lens)
+            lens += 1
+            for f in (lambda: fa.decode_fp8(q, *cache, lens), lambda: fa.decode_fp8(q, *cache, long_lens),
+                      lambda: fa.decode_shared_prefix(q, kp, vp, cache[0], cache[1], lens, cache[2], cache[3]),
+                      lambda: fa.fp8_cache_read(*cache, lens, 20, torch.float16)):
+                o = f()
+                outs += [t.clone() for t in o]
+                for t in o:
+                    t.fill_(7)
+                if wait:
+                    torch.cuda.synchronize()
+            x.zero_()
+            q.zero_()
+        torch.cuda.synchronize()
+        return outs
+
+    ref = chain(True)
+    for _ in range(3):
+        for a, b in zip(ref, chain(False)):
+            assert torch.equal(torch.nan_to_num(a.float(), nan=-3.0), torch.nan_to_num(b.float(), nan=-3.0))
+    done(fa)
+
+
+class Guarded:
+    """A tensor between two stretches of sentinel bytes."""
+    PAD = 64 * 1024
+
+    def __init__(self, shape, dtype, fill=None):
+        self.n = math.prod(shape) * torch.empty((), dtype=dtype).element_size()
+        self.buf = torch.full((2 * self.PAD + (self.n + 15) // 16 * 16,), 0xA5, dtype=torch.uint8, device="cuda")
+        self.t = self.buf[self.PAD:self.PAD + self.n].view(dtype).view(shape)
+        if fill is not None:
+            self.t.copy_(fill)
+
+    def intact(self):
+        return bool((self.buf[:self.PAD] == 0xA5).all()) and bool((self.buf[self.PAD + self.n:] == 0xA5).all())
+
+
+@pytest.mark.parametrize("B,Hq,Hkv,N,d,dt", [(3, 6, 2, 133, 64, "fp16"), (2, 16, 1, 70, 128, "bf16"),
+                                             (150, 12, 3, 190, 64, "bf16"), (1, 5, 5, 1, 128, "fp16"),
+                                             (2, 8, 2, 9000, 64, "fp16")])
+def test_everything_stays_inside_its_outputs(fa, B, Hq, Hkv, N, d, dt):
+    t = DT[dt]
+    q, k, v = (Guarded((B, 3, H, d), t, normal((B, 3, H, d), t, 131 + i).cuda())
+               for i, H in enumerate((Hq, Hkv, Hkv)))
+    qo, ko = Guarded((B, 3, Hq, d), t), Guarded((B, 3, Hkv, d), t)
+    fa.rotary_fwd(q.t, k.t, torch.arange(3, dtype=torch.int32, device="cuda"), fa.rotary_table(32), q_out=qo.t,
+                  k_out=ko.t)
+    raw = empty_cache(B, N, Hkv, d)
+    cache = [Guarded(c.shape, c.dtype, torch.nan_to_num(c, nan=0.5) if c.is_floating_point() else c & 0x77) for c in raw]
+    fa.fp8_cache_append(ko.t, v.t, *(c.t for c in cache), ints([N - 1 - b % 3 for b in range(B)]))
+    lens = ints([(N - b * 13) % (N + 1) for b in range(B)])
+    rows = [Guarded((B, N, Hkv, d), t) for _ in range(2)]
+    from exact_io_aware_80_b200 import _lib
+    stream = torch.cuda.current_stream().cuda_stream
+    code = _lib.FA_BF16 if dt == "bf16" else _lib.FA_FP16
+    _lib.fa_fp8_cache_read(*(c.t.data_ptr() for c in cache), lens.data_ptr(), rows[0].t.data_ptr(),
+                           rows[1].t.data_ptr(), B, N, Hkv, N, d, code, stream)
+    q1 = Guarded((B, 1, Hq, d), t, qo.t[:, :1])
+    kp = Guarded((1, 333, Hkv, d), t, normal((1, 333, Hkv, d), t, 141).cuda())
+    everything = [q, k, v, qo, ko, q1, kp] + cache + rows
+    for splits in (0, 1, 3):
+        need = fa.fa_decode_fp8_workspace_bytes(B, Hq, Hkv, N, splits, d)
+        ws = Guarded((max(need, 16),), torch.uint8)
+        o, lse = Guarded((B, 1, Hq, d), t), Guarded((B, Hq, 1), torch.float32)
+        if splits == 0:
+            fa.decode_fp8(q1.t, *(c.t for c in cache), lens, workspace=ws.t, out=o.t, lse=lse.t)
+        else:
+            fa.decode_shared_prefix(q1.t, kp.t, kp.t, cache[0].t, cache[1].t, lens, cache[2].t, cache[3].t,
+                                    prefix_splits=splits, workspace=ws.t, out=o.t, lse=lse.t)
+            o16, l16 = Guarded((B, 1, Hq, d), t), Guarded((B, Hq, 1), torch.float32)
+            fa.decode_shared_prefix(q1.t, kp.t, kp.t, rows[0].t, rows[1].t, lens, prefix_splits=splits,
+                                    workspace=ws.t, out=o16.t, lse=l16.t)
+            everything += [o16, l16]
+        everything += [ws, o, lse]
+    done(fa)
+    assert all(g.intact() for g in everything)
+    assert all(torch.isfinite(g.t.float()).all() for g in (qo, ko, *rows))
+
+
 @pytest.mark.slow
 def test_decode_fp8_past_two_gigabytes_of_codes(fa):
     """Offsets beyond 2^31: three sequences of 2^20 - 5 keys, 8 heads of 128, sampled heads of the last."""
