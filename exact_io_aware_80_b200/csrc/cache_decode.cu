@@ -677,43 +677,32 @@ __global__ void __launch_bounds__(kThreads, cache_ctas_per_sm(D, F8, NB == 2)) c
   if (blockIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-// Merge: WARPS warps per (h_q, b), each over its share of the row's partials: the prefix's splits, then
-// the cache's slots.  Every warp first takes all their LSE (a lane each, 32 at a time) to the shared
-// maximum; the sums' loads then do not depend on one another.
+// Merge: WARPS warps per (h_q, b), each over every WARPS-th of the row's partials (the prefix's splits,
+// then the cache's slots): the first kAhead of them, all loaded together, then one by one.
+constexpr int kAhead = 8;
 constexpr int combine_threads(int warps) { return warps > 4 ? 32 * warps : 128; }
 template <typename T, int D, int WARPS>
 __global__ void __launch_bounds__(combine_threads(WARPS)) cache_combine_kernel(CacheDecodeArgs p) {
   __shared__ float red[WARPS][D];
-  __shared__ float red_l[WARPS];
+  __shared__ float red_m[WARPS], red_l[WARPS];
   constexpr int kCols = D / 32;  // columns per lane
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = warp % WARPS;
   const long row = (long)blockIdx.x * (combine_threads(WARPS) / 32 / WARPS) + warp / WARPS;  // b Hq + h
   const long nrows = (long)p.B * p.Hq;
+  if (WARPS == 1 && row >= nrows) return;
   const int Sp = p.prefix_splits, G = p.Hq / p.Hkv;
   const int b = (int)(row / p.Hq), h = (int)(row - (long)b * p.Hq), hk = h / G;
-  const bool has = row < nrows && p.seqlens[row < nrows ? b : 0] > 0 && p.Nk_max > 0;
+  const bool has = p.seqlens[b] > 0;
   // (no early start for what follows: the next pass's CTAs, taking their places among this kernel's,
   // came to lie unevenly on the SMs and cost 3 % of a long decode)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int2 span = has ? p.spans[b] : make_int2(0, -1);
-  const int live = row < nrows ? Sp + span.y - span.x + 1 : 0;
+  const int live = Sp + span.y - span.x + 1;
   const long slot0 = ((long)hk * (p.B + p.cache_ctas / p.Hkv) + b + span.x) * G + (h - hk * G);  // then G apart
   auto lse_of = [&](int s) { return s < Sp ? p.lse_part[row * Sp + s] : p.lse_cache[slot0 + (long)(s - Sp) * G]; };
-  float mx = -INFINITY;
-  for (int s = lane; s < live; s += 32) mx = fmaxf(mx, lse_of(s));
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  const float mu = mx == -INFINITY ? 0.f : mx;
-  float l = 0.f;
-  float o[kCols];
-#pragma unroll
-  for (int i = 0; i < kCols; ++i) o[i] = 0.f;
-#pragma unroll 8
-  for (int s = part; s < live; s += WARPS) {
-    const float w = ex2((lse_of(s) - mu) * kLog2e);
+  auto load = [&](int s, float (&x)[kCols]) {
     const float* src =
         (s < Sp ? p.o_part + (row * Sp + s) * D : p.o_cache + (slot0 + (long)(s - Sp) * G) * D) + lane * kCols;
-    float x[kCols];
     if constexpr (D == 128) {
       const float4 f = *reinterpret_cast<const float4*>(src);
       x[0] = f.x;
@@ -725,34 +714,76 @@ __global__ void __launch_bounds__(combine_threads(WARPS)) cache_combine_kernel(C
       x[0] = f.x;
       x[1] = f.y;
     }
+  };
+  float lse[kAhead], x[kAhead][kCols];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) {
+    const int s = part + i * WARPS;
+    lse[i] = -INFINITY;
+#pragma unroll
+    for (int c = 0; c < kCols; ++c) x[i][c] = 0.f;
+    if (s < live) {
+      lse[i] = lse_of(s);
+      load(s, x[i]);
+    }
+  }
+  float mx = lse[0];
+#pragma unroll
+  for (int i = 1; i < kAhead; ++i) mx = fmaxf(mx, lse[i]);
+  float l = 0.f, o[kCols];
+#pragma unroll
+  for (int c = 0; c < kCols; ++c) o[c] = 0.f;
+  auto add = [&](float v, const float (&y)[kCols], float mu) {
+    const float w = ex2((v - mu) * kLog2e);
     l += w;
 #pragma unroll
-    for (int i = 0; i < kCols; ++i) o[i] += w * x[i];
+    for (int c = 0; c < kCols; ++c) o[c] += w * y[c];
+  };
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) add(lse[i], x[i], mx == -INFINITY ? 0.f : mx);
+  for (int s = part + kAhead * WARPS; s < live; s += WARPS) {
+    const float v = lse_of(s);
+    load(s, x[0]);
+    if (v > mx) {
+      const float corr = mx == -INFINITY ? 1.f : ex2((mx - v) * kLog2e);  // l and O are 0 or NaN without a maximum
+      mx = v;
+      l *= corr;
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) o[c] *= corr;
+    }
+    add(v, x[0], mx == -INFINITY ? 0.f : mx);
   }
   if constexpr (WARPS > 1) {
 #pragma unroll
-    for (int i = 0; i < kCols; ++i) red[warp][lane * kCols + i] = o[i];
-    if (lane == 0) red_l[warp] = l;
+    for (int c = 0; c < kCols; ++c) red[warp][lane * kCols + c] = o[c];
+    if (lane == 0) {
+      red_m[warp] = mx;
+      red_l[warp] = l;
+    }
     __syncthreads();
-    if (warp > 0) return;
+    const int first = warp - part;  // this row's warps: first .. first + WARPS - 1
+    if (part > 0) return;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) mx = fmaxf(mx, red_m[first + w]);
     l = 0.f;
 #pragma unroll
-    for (int i = 0; i < kCols; ++i) o[i] = 0.f;
+    for (int c = 0; c < kCols; ++c) o[c] = 0.f;
 #pragma unroll
     for (int w = 0; w < WARPS; ++w) {
-      l += red_l[w];
+      const float m = red_m[first + w], f = m == -INFINITY ? 1.f : ex2((m - mx) * kLog2e);
+      l += f * red_l[first + w];
 #pragma unroll
-      for (int i = 0; i < kCols; ++i) o[i] += red[w][lane * kCols + i];
+      for (int c = 0; c < kCols; ++c) o[c] += f * red[first + w][lane * kCols + c];
     }
   }
-  if (row >= nrows) return;
   const float inv = 1.f / l;
 #pragma unroll
-  for (int i = 0; i < kCols; ++i) o[i] = l == 0.f ? 0.f : o[i] * inv;  // no key: O = 0, LSE = -inf
+  for (int c = 0; c < kCols; ++c) o[c] = l == 0.f ? 0.f : o[c] * inv;  // no key: O = 0, LSE = -inf
+  if (!FA_IN_BOUNDS(p.status, row, nrows)) return;
   uint32_t* go = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o) + row * D + lane * kCols);
 #pragma unroll
-  for (int i = 0; i < kCols / 2; ++i) go[i] = Elem<T>::pack(o[2 * i], o[2 * i + 1]);
-  if (lane == 0) p.lse[row] = mu + logf(l);
+  for (int c = 0; c < kCols / 2; ++c) go[c] = Elem<T>::pack(o[2 * c], o[2 * c + 1]);
+  if (lane == 0) p.lse[row] = (mx == -INFINITY ? 0.f : mx) + logf(l);
 }
 
 template <typename T, int D, bool F8, int NB, bool REST>
