@@ -679,25 +679,27 @@ __global__ void __launch_bounds__(kThreads, cache_ctas_per_sm(D, F8, NB == 2)) c
 
 // Merge: WARPS warps per (h_q, b), each over every WARPS-th of the row's partials (the prefix's splits,
 // then the cache's slots): the first kAhead of them, all loaded together, then one by one.
-constexpr int kAhead = 8;
 constexpr int combine_threads(int warps) { return warps > 4 ? 32 * warps : 128; }
 template <typename T, int D, int WARPS>
 __global__ void __launch_bounds__(combine_threads(WARPS)) cache_combine_kernel(CacheDecodeArgs p) {
-  __shared__ float red[WARPS][D];
-  __shared__ float red_m[WARPS], red_l[WARPS];
+  constexpr int kWarps = combine_threads(WARPS) / 32;
+  __shared__ float red[kWarps][D];
+  __shared__ float red_m[kWarps], red_l[kWarps];
   constexpr int kCols = D / 32;  // columns per lane
+  constexpr int kAhead = WARPS <= 2 ? 8 : 4;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = warp % WARPS;
-  const long row = (long)blockIdx.x * (combine_threads(WARPS) / 32 / WARPS) + warp / WARPS;  // b Hq + h
+  const long row = (long)blockIdx.x * (kWarps / WARPS) + warp / WARPS;  // b Hq + h
   const long nrows = (long)p.B * p.Hq;
   if (WARPS == 1 && row >= nrows) return;
+  const bool any = row < nrows;  // (two warps a row: an odd number of rows leaves two without)
   const int Sp = p.prefix_splits, G = p.Hq / p.Hkv;
   const int b = (int)(row / p.Hq), h = (int)(row - (long)b * p.Hq), hk = h / G;
-  const bool has = p.seqlens[b] > 0;
+  const bool has = any && p.seqlens[any ? b : 0] > 0;
   // (no early start for what follows: the next pass's CTAs, taking their places among this kernel's,
   // came to lie unevenly on the SMs and cost 3 % of a long decode)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int2 span = has ? p.spans[b] : make_int2(0, -1);
-  const int live = Sp + span.y - span.x + 1;
+  const int live = any ? Sp + span.y - span.x + 1 : 0;
   const long slot0 = ((long)hk * (p.B + p.cache_ctas / p.Hkv) + b + span.x) * G + (h - hk * G);  // then G apart
   auto lse_of = [&](int s) { return s < Sp ? p.lse_part[row * Sp + s] : p.lse_cache[slot0 + (long)(s - Sp) * G]; };
   auto load = [&](int s, float (&x)[kCols]) {
@@ -762,7 +764,7 @@ __global__ void __launch_bounds__(combine_threads(WARPS)) cache_combine_kernel(C
     }
     __syncthreads();
     const int first = warp - part;  // this row's warps: first .. first + WARPS - 1
-    if (part > 0) return;
+    if (part > 0 || !any) return;
 #pragma unroll
     for (int w = 0; w < WARPS; ++w) mx = fmaxf(mx, red_m[first + w]);
     l = 0.f;
@@ -820,12 +822,14 @@ cudaError_t launch_combine(const CacheDecodeArgs& a, cudaStream_t s) {
   const long rows = (long)a.B * a.Hq;
   // the more warps a row the more partials it may have, and the fewer rows there are to fill the SMs
   const long parts = a.prefix_splits + a.cache_ctas / ((long)a.B * a.Hkv);
-  const int warps = parts > 16 && rows <= 4l * device_sm_count() ? 16 : parts > 8 || rows < 4l * device_sm_count() ? 4 : 1;
+  const bool few = rows <= 4l * device_sm_count();
+  const int warps = few ? (parts > 16 ? 16 : 4) : parts > 8 ? 2 : 1;
   const int per = combine_threads(warps) / 32 / warps;  // rows a CTA
   const long ctas = (rows + per - 1) / per;
   if (ctas > 0x7fffffffL) return cudaErrorInvalidValue;
   auto kern = warps == 16 ? cache_combine_kernel<T, D, 16>
               : warps == 4 ? cache_combine_kernel<T, D, 4>
+              : warps == 2 ? cache_combine_kernel<T, D, 2>
                            : cache_combine_kernel<T, D, 1>;
   return launch_dependent(kern, dim3((unsigned)ctas), combine_threads(warps), 0, s, a);
 }

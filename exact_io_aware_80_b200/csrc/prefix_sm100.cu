@@ -525,7 +525,7 @@ cudaError_t launch(const CacheDecodeArgs& a, cudaStream_t s) {
   constexpr int smem = Smem<D, NT, REST>::kBytes;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  const int grid = (int)std::min<long long>(work, device_sm_count());
+  const int grid = (int)std::min<long long>(work, a.prefix_ctas);
   return launch_dependent(kern, dim3(grid), Smem<D, NT, REST>::kThreads, smem, s, mq, mk, mv, mo, p);
 }
 

@@ -125,6 +125,7 @@ struct CacheDecodeArgs {
   int B, Hq, Hkv, Np, Nk_max, d;
   int prefix_splits, prefix_chunk;  // keys per prefix split, a multiple of 128
   int after_prefix;                 // the launch before the cache kernel's is the prefix kernel's
+  int prefix_ctas;                  // CTAs that take the prefix's work in turn
   int solo;                         // > 0: CTAs of a cluster per sequence and KV head, which merge alone
   int cache_ctas;                   // a multiple of Hkv, at most max(kMaxCacheCtas, Hkv)
   float scale;

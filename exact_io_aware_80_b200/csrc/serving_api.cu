@@ -100,6 +100,38 @@ long long prefix_row_blocks(int B, int G) {
   return B <= seqs ? 1 : (B + 2 * seqs - 1) / (2 * seqs);
 }
 
+// CTAs of the prefix kernel for a number of splits, and an estimate of the call's time in microseconds.
+// As measured: a K/V tile takes 2 with two query tiles, 1.6 with one, a work 4 more in its turn and the
+// kernel 5 to start and end; beside it an SM streams 60 KB of a 16-bit cache, 40 KB of an E4M3 one; four fifths
+// of a cache's room are taken to be in use.  The cache kernel fills the SMs that the prefix leaves, if they
+// are a quarter at least, or follows it, which costs 8 and a third of its time more.  64 sequences behind
+// 32768 keys, 1024 of their own: 80 CTAs 65 us, 144 79; 250 behind 8192, 512: 64 CTAs 73 us, 128 87.
+struct PrefixPlan {
+  int ctas;
+  double cost;
+};
+PrefixPlan plan_prefix(int B, int G, int Hkv, int Np, int Nk_max, int d, bool fp8, int splits, int sms) {
+  const long long work = prefix_row_blocks(B, G) * Hkv * splits;
+  const int per = ((Np + 127) / 128 + splits - 1) / splits;  // K/V tiles of a work
+  const double tile = B > 128 / G ? 2.0 : 1.6;
+  const double kb = 0.8 * 2.0 * B * Nk_max * Hkv * (fp8 ? d + 4 : 2 * d) / 1e3;
+  const double cache = kb / (fp8 ? 40 : 60);  // SM microseconds
+  const double hbm = (kb + 4.0 * Np * Hkv * d / 1e3) / 6500.0;
+  PrefixPlan best{0, 0};
+  for (int rounds = 1; rounds <= 8; ++rounds) {
+    const long long ctas = (work + rounds - 1) / rounds;
+    if (ctas > sms) continue;
+    const double prefix = rounds * (per * tile + 4.0) + 5.0, left = (double)(sms - ctas);
+    const double cost = std::max(hbm, left >= sms / 4 ? std::max(prefix, cache / left) : prefix + 1.3 * cache / sms + 8.0);
+    if (best.ctas == 0 || cost < best.cost) best = PrefixPlan{(int)ctas, cost};
+  }
+  if (best.ctas == 0) {
+    const long long rounds = (work + sms - 1) / sms;
+    best = PrefixPlan{sms, std::max(hbm, rounds * (per * tile + 4.0) + 5.0 + 1.3 * cache / sms + 8.0)};
+  }
+  return best;
+}
+
 }  // namespace
 
 extern "C" {
@@ -263,24 +295,13 @@ static int prefix_chunk(int Np, int splits) { return ((Np + splits - 1) / splits
 
 int fa_decode_prefix_splits(int B, int Hq, int Hkv, int Np, int Nk_max, int d, int fp8_cache, int num_sms) {
   if (B < 1 || Hq < 1 || Hkv < 1 || Np < 1 || Nk_max < 0 || d < 1 || Hq % Hkv != 0 || Hq / Hkv > 128) return 1;
-  const int sms = sm_count(num_sms), tiles = (Np + 127) / 128;
-  const long long units = prefix_row_blocks(B, Hq / Hkv) * Hkv;
-  // Microseconds, as measured: a K/V tile takes 2 with two query tiles, 1.6 with one, a work 8 to start
-  // and end, and an SM streams 65 KB of cache.  The cache kernel fills the SMs that the prefix leaves, or
-  // follows it, which costs 8 and a third of its time more.  64 sequences behind 32768 keys, 1024 of
-  // their own: 10 splits (80 CTAs) 65 us, 18 (144) 79; 250 behind 8192, 512: 2 (64) 74 us, 4 (128) 87.
-  const double tile = B > 128 / (Hq / Hkv) ? 2.0 : 1.6;
-  const double cache = 2.0 * B * Nk_max * Hkv * (fp8_cache ? d + 4 : 2 * d) / 65e3;  // SM microseconds
+  const int tiles = (Np + 127) / 128;
   int best = 1;
   double least = -1;
   for (int s = 1; s <= std::min(tiles, 256); ++s) {
     const int per = (tiles + s - 1) / s;
     if ((tiles + per - 1) / per != s) continue;  // the same lengths with fewer splits
-    const long long work = units * s;
-    const double prefix = (double)((work + sms - 1) / sms) * (per * tile + 8.0);
-    const double left = sms - (double)std::min<long long>(work, sms);
-    const double both = left >= sms / 4 ? std::max(prefix, cache / left) : prefix + 1.3 * cache / sms + 8.0;
-    const double cost = both + 0.1 * s;  // and every split a partial to merge
+    const double cost = plan_prefix(B, Hq / Hkv, Hkv, Np, Nk_max, d, fp8_cache != 0, s, sm_count(num_sms)).cost + 0.1 * s;
     if (least < 0 || cost < least) {
       least = cost;
       best = s;
@@ -332,8 +353,8 @@ fa_status fa_decode_shared_prefix(const void* q, const void* k_prefix, const voi
   a.prefix_chunk = pchunk;
   a.solo = solo_of(B, Hkv, Nk_max, prefix_splits);
   const int sms = fa::device_sm_count();
-  const long long work = prefix_row_blocks(B, Hq / Hkv) * Hkv * prefix_splits;
-  a.cache_ctas = cache_ctas_of(B, Hkv, Nk_max, d, Hq / Hkv, k_scale != nullptr, sms, std::min<long long>(work, sms));
+  a.prefix_ctas = plan_prefix(B, Hq / Hkv, Hkv, Np, Nk_max, d, k_scale != nullptr, prefix_splits, sms).ctas;
+  a.cache_ctas = cache_ctas_of(B, Hkv, Nk_max, d, Hq / Hkv, k_scale != nullptr, sms, a.prefix_ctas);
   a.scale = scale;
   a.bf16 = dt == FA_BF16 ? 1 : 0;
   a.status = fa::device_status_word();
