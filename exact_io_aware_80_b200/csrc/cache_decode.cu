@@ -52,6 +52,9 @@
 //  * the weights p_j s^v_j are fp16 in units of 2^(e - 8), where 2^e exceeds
 //    every s^v seen so far: at most 2^14 (p up to 2^6), relative error 2^-11
 //    down to 2^-22 of 2^e, absolute 2^-33 of it below.
+// Measured (bf16, 32 query and 8 KV heads of 128): 64 sequences of up to 32768 keys, 3.34 GB, 496 us
+// with the merge, 6.7 TB/s or 1.03 of a plain copy; one of 32768 18.2 us; 16 of up to 2000 15.3 us.
+//
 // l sums the unrounded p_j.  fp16 weights of a 16-bit cache are kept 2^8 larger
 // (m lowered by 8) for the same reason: at most 2^14, normal down to 2^-22.
 #include <math.h>
@@ -77,7 +80,8 @@ constexpr int kMinUnit = -112;  // smallest e of the weights' unit (all powers o
 
 // A warp's two buffers of kStep keys each.  Two of them (99 KB in flight on an SM of three CTAs) leave
 // room for a third CTA: three of 32 keys were 2 % slower on 32768-key sequences and up to 30 % on
-// short ones.
+// short ones.  E4M3 rows of 128 values, 64 sequences of 32768 keys and 16 of 2000: 32 keys and three CTAs an
+// SM 496 and 15.3 us, 16 keys and four CTAs (128 registers) 500 and 19.2, 16 keys and three 528 and 19.1.
 template <int D, bool F8>
 struct Ring {
   static constexpr int kRow = D * (F8 ? 1 : 2);          // bytes of a K or V row
@@ -193,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, cache_ctas_per_sm(D, F8, NB == 2)) c
   const long row_bytes = (long)p.Hkv * R::kRow;
 
   // W, this CTA's part [begin, end) of the line, and the sequence that begin lies in.  Every warp for
-// itself: a lane sums the blocks of a stretch of sequences, and the one whose stretch holds begin walks it
+  // itself: a lane sums the blocks of a stretch of sequences, and the one whose stretch holds begin walks it
   auto length = [&](int b) { return min(max(p.seqlens[b], 0), p.Nk_max); };
   auto blocks = [&](int n) { return (n + kBlock - 1) / kBlock; };
   int begin, end, W = 0, C = 0;  // W < 2^31: a block of a head takes 4 KB at least
@@ -820,7 +824,9 @@ cudaError_t launch_part_d(const CacheDecodeArgs& a, cudaStream_t s) {
 template <typename T, int D>
 cudaError_t launch_combine(const CacheDecodeArgs& a, cudaStream_t s) {
   const long rows = (long)a.B * a.Hq;
-  // the more warps a row the more partials it may have, and the fewer rows there are to fill the SMs
+  // The more warps a row the more partials it may have, and the fewer rows there are to fill the SMs.  As
+  // measured, us a call with 1, 2, 4 and 16 warps: 32 rows of 55 partials 32.7, 22.1, 20.1, 18.3; 512 of 4 47.4,
+  // 47.4, 47.3, 49.0; 2048 of 12 57.1, 54.9, 54.3, 65.2; 8000 of 3 35.6, 39.0, 41.9, 78.9.
   const long parts = a.prefix_splits + a.cache_ctas / ((long)a.B * a.Hkv);
   const bool few = rows <= 4l * device_sm_count();
   const int warps = few ? (parts > 16 ? 16 : 4) : parts > 8 ? 2 : 1;

@@ -12,6 +12,10 @@
 // MFLOP on the tensor cores and 32768 exponentials; by the tensor cores and the
 // exponentials beyond, when several row blocks read one tile from L2.
 //
+// Measured (bf16, 32 query and 8 KV heads of 128), the whole call with the sequences' own caches and the
+// merge: 64 sequences behind 32768 keys with up to 1024 of their own, 337 MB and 35 GFLOP, 63.5 us, 5.3
+// TB/s or 0.81 of a plain copy; 250 behind 8192 with up to 512 E4M3 ones, 240 MB and 35 GFLOP, 72.9 us.
+//
 // The machinery is the forward kernel's (fwd_sm100.cu): a persistent CTA per
 // SM; one or two 128-row query tiles; one thread issuing TMA loads of K and V
 // into a two-stage ring, one issuing tcgen05 MMAs with S, P and O in TMEM, and

@@ -351,6 +351,7 @@ PREFIX = [
     (120, 8, 4, 600, 130, 64, "fp16", True, 3),       # the caches merged apart
     (60, 8, 8, 200, 30, 128, "bf16", False, None),
     (2, 8, 2, 1500, 30, 64, "bf16", True, 12),        # many prefix splits
+    (67, 9, 3, 1100, 40, 64, "fp16", False, 9),       # 603 rows of nine splits and more
     (40, 14, 2, 260, 9, 64, "bf16", False, 1),        # G = 7: 18 sequences a tile, 126 rows
 ]
 
