@@ -15,9 +15,10 @@
 // Bound by HBM: 2 d bytes in and d + 4 out per appended row, d + 4 in and 2 d
 // out per row read back.  A thread takes 16 values (two 16-byte loads, one
 // 16-byte store of codes), so d / 16 threads hold a row and its maximum is
-// log2(d / 16) shuffles.  Measured: 24003 tokens, a third of them past their
-// counts, of 8 heads of 64, 50 MB, 12.1 us, 4.1 TB/s, bound by the issue slots
-// (71 % used) that the exact quotients take; 65536 tokens of 8 heads of 128 read
+// log2(d / 16) shuffles.  Measured: 64000 tokens of 8 heads of 128 appended, 397
+// MB, 66.5 us, 6.0 TB/s or 0.92 of a plain copy; 24003 tokens, a third of them
+// past their counts, of 8 heads of 64, 50 MB, 10.5 us, 4.8 TB/s, where the issue
+// slots that the exact quotients take weigh more; 65536 tokens of 8 heads of 128 read
 // back, 407 MB, 62 to 69 us with where the buffers lie, 6.6 to 5.9 TB/s.
 #include "common.cuh"
 #include "kernels.h"
@@ -88,52 +89,62 @@ __device__ __forceinline__ uint4 codes16(const float2 (&n)[8], float s) {
                     half[6] | (half[7] << 16));
 }
 
-// grid: (row groups, 2); y = 0 appends K rows, 1 V rows.  D / 16 consecutive threads hold a row.
-template <typename T, int D>
+// D / 16 consecutive threads hold a row.  TENSORS = 2: K's and V's, which share the arithmetic of its place;
+// 1: one of them, by blockIdx.y.
+template <typename T, int D, int TENSORS>
 __global__ void __launch_bounds__(kThreads) append_kernel(Fp8CacheArgs p, Rows rows) {
   wait_for_earlier_grids();
   constexpr int kUnits = D / 16;
-  const bool isv = blockIdx.y != 0;
   const uint32_t r = blockIdx.x * (kThreads / kUnits) + threadIdx.x / kUnits;
   const int unit = threadIdx.x % kUnits;
-  uint8_t* codes = nullptr;
-  float* scale = nullptr;
-  uint4 w[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+  auto is_v = [&](int t) { return TENSORS == 2 ? t != 0 : blockIdx.y != 0; };
+  long crow = -1, srow = 0;  // places of the codes and of the scale
+  uint4 w[TENSORS][2] = {};
   if (r < rows.count) {
     const Row at = row_at(rows, r);
     const long dst = (long)p.start[at.b] + at.i;
     if ((int)at.i < (p.counts ? p.counts[at.b] : p.n) && dst >= 0 && dst < p.Nk_max) {
-      const long bs = isv ? p.v_bs : p.k_bs, ts = isv ? p.v_ts : p.k_ts;
-      const long in = at.b * bs + at.i * ts + (long)(at.h * D);
-      const long crow = ((long)at.b * p.Nk_max + dst) * p.Hkv + at.h;
-      const long srow = ((long)at.b * p.Hkv + at.h) * p.Nk_max + dst;
-      if (FA_IN_BOUNDS(p.status, in + D - 1, (p.B - 1) * bs + (p.n - 1) * ts + (long)p.Hkv * D) &&
-          FA_IN_BOUNDS(p.status, crow, (long)p.B * p.Nk_max * p.Hkv) &&
-          FA_IN_BOUNDS(p.status, srow, (long)p.B * p.Nk_max * p.Hkv)) {
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(isv ? p.v : p.k) + in) + 2 * unit;
-        w[0] = src[0];
-        w[1] = src[1];
-        codes = (isv ? p.v8 : p.k8) + crow * D;
-        scale = (isv ? p.v_scale : p.k_scale) + srow;
+      const long c = ((long)at.b * p.Nk_max + dst) * p.Hkv + at.h;
+      srow = ((long)at.b * p.Hkv + at.h) * p.Nk_max + dst;
+      if (FA_IN_BOUNDS(p.status, c, (long)p.B * p.Nk_max * p.Hkv) &&
+          FA_IN_BOUNDS(p.status, srow, (long)p.B * p.Nk_max * p.Hkv))
+        crow = c;
+#pragma unroll
+      for (int t = 0; t < TENSORS; ++t) {
+        const long bs = is_v(t) ? p.v_bs : p.k_bs, ts = is_v(t) ? p.v_ts : p.k_ts;
+        const long in = at.b * bs + at.i * ts + (long)(at.h * D);
+        if (FA_IN_BOUNDS(p.status, in + D - 1, (p.B - 1) * bs + (p.n - 1) * ts + (long)p.Hkv * D)) {
+          const uint4* src =
+              reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(is_v(t) ? p.v : p.k) + in) + 2 * unit;
+          w[t][0] = src[0];
+          w[t][1] = src[1];
+        } else {
+          crow = -1;
+        }
       }
     }
   }
-  const uint32_t u[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
-  uint32_t most = u[0] & 0x7FFF7FFFu;
+  // rows past their counts (a third of three prompts of up to 8001 tokens: 10.5 us with this, 10.8 without)
+  if (!__any_sync(0xffffffffu, crow >= 0)) return;
 #pragma unroll
-  for (int i = 1; i < 8; ++i) most = max2_nan<T>(most, u[i] & 0x7FFF7FFFu);
-  const float2 both = Elem<T>::unpack(most);
-  float amax = max_nan(both.x, both.y);
+  for (int t = 0; t < TENSORS; ++t) {
+    const uint32_t u[8] = {w[t][0].x, w[t][0].y, w[t][0].z, w[t][0].w, w[t][1].x, w[t][1].y, w[t][1].z, w[t][1].w};
+    uint32_t most = u[0] & 0x7FFF7FFFu;
 #pragma unroll
-  for (int o = D / 32; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  const float s = amax == 0.f ? 1.f : __fdiv_rn(amax, 448.f);
-  float2 n[8];
+    for (int i = 1; i < 8; ++i) most = max2_nan<T>(most, u[i] & 0x7FFF7FFFu);
+    const float2 both = Elem<T>::unpack(most);
+    float amax = max_nan(both.x, both.y);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) n[i] = Elem<T>::unpack(u[i] ^ 0x80008000u);
-  if (codes) {
-    *reinterpret_cast<uint4*>(codes + 16 * unit) =
-        s >= 0x1p-90f && s <= 0x1p90f ? codes16<true>(n, s) : codes16<false>(n, s);
-    if (unit == 0) *scale = s;
+    for (int o = D / 32; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    const float s = amax == 0.f ? 1.f : __fdiv_rn(amax, 448.f);
+    float2 n[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) n[i] = Elem<T>::unpack(u[i] ^ 0x80008000u);
+    if (crow >= 0) {
+      reinterpret_cast<uint4*>((is_v(t) ? p.v8 : p.k8) + crow * D)[unit] =
+          s >= 0x1p-90f && s <= 0x1p90f ? codes16<true>(n, s) : codes16<false>(n, s);
+      if (unit == 0) (is_v(t) ? p.v_scale : p.k_scale)[srow] = s;
+    }
   }
 }
 
@@ -196,8 +207,11 @@ Rows rows_of(const Fp8CacheArgs& a) { return Rows{(uint32_t)a.B * a.n * a.Hkv, F
 template <typename T, int D>
 cudaError_t launch_append(const Fp8CacheArgs& a, cudaStream_t s) {
   const Rows rows = rows_of(a);
-  const uint32_t per = kThreads / (D / 16);
-  return launch_dependent(append_kernel<T, D>, dim3((rows.count + per - 1) / per, 2), kThreads, 0, s, a, rows);
+  const uint32_t per = kThreads / (D / 16), groups = (rows.count + per - 1) / per;
+  // 64000 tokens of 8 heads of 128: 66.5 us with K and V in a thread, 75.6 apart; 2048: 3.9 and 3.6; 64: 2.1 and 1.7
+  if (groups < 4u * device_sm_count())
+    return launch_dependent(append_kernel<T, D, 1>, dim3(groups, 2), kThreads, 0, s, a, rows);
+  return launch_dependent(append_kernel<T, D, 2>, dim3(groups), kThreads, 0, s, a, rows);
 }
 template <typename T, int D, int ROWS>
 cudaError_t launch_read_rows(const Fp8CacheArgs& a, const Rows& rows, cudaStream_t s) {

@@ -160,6 +160,8 @@ APPEND = [
     (4, 33, 3, 64, 40, "bf16", [0, 5, 7, 3], [33, 0, 1, 20]),
     (2, 70, 8, 128, 100, "fp16", [30, 0], [70, 69]),
     (3, 9, 5, 128, 12, "bf16", [-4, 8, 12], [9, 99, -3]),  # partly outside the cache, counts clamped
+    (3, 1700, 8, 64, 2000, "fp16", [250, 0, 1999], [1700, 333, 1]),  # enough rows to take K and V together
+    (2, 1300, 8, 128, 1400, "bf16", [-7, 101], None),
 ]
 
 
