@@ -14,7 +14,9 @@
 // each KV head, CTA i takes the blocks from i W / C to (i + 1) W / C, whatever
 // sequences they belong to, and leaves one partial (O, LSE of the group's rows) per
 // sequence that it touches, in its head's slot b + i -- along the line either
-// summand grows, so no two partials share one.  Every CTA has the same keys to read
+// summand grows, so no two partials share one; a sequence that one CTA has whole, without
+// a prefix, goes straight to the outputs (1000 sequences of up to 1000 keys: 259 us, 269 through the merge; for
+// groups of 9 to 16 heads, whose CTAs have no register left, 500 of 700 36.2 and 35.9, so they do not).  Every CTA has the same keys to read
 // however ragged the batch, and the CTAs of the Hkv heads, neighbours in the grid,
 // read the same tokens' rows together (a line through the heads as well, whose CTAs
 // stand at different tokens, lost 13 % of the bandwidth).
@@ -599,6 +601,7 @@ __global__ void __launch_bounds__(kThreads, cache_ctas_per_sm(D, F8, NB == 2)) c
     __syncthreads();
     const long slots = (long)p.Hkv * (p.B + gridDim.x / p.Hkv);
     const long slot = (long)hk * (p.B + gridDim.x / p.Hkv) + cur.b + cta;
+    const bool straight = !SOLO && NB == 1 && p.prefix_splits == 0 && cur.blk == 0 && cur.pos + cur.blks <= end;
     // whoever has a sequence's first block knows which CTAs have the others
     if (!SOLO && tid == 0 && cur.blk == 0 && hk == 0 && FA_IN_BOUNDS(p.status, cur.b, p.B))
       p.spans[cur.b] = make_int2(cta, (int)(((long long)(cur.pos + cur.blks) * C - 1) / W));
@@ -627,6 +630,13 @@ __global__ void __launch_bounds__(kThreads, cache_ctas_per_sm(D, F8, NB == 2)) c
       if constexpr (SOLO) {
         *reinterpret_cast<float4*>(solo_o + idx) = part;
         if (idx % D == 0) solo_lse[g] = lse;
+      } else if (straight) {
+        const long row = (long)cur.b * p.Hq + (long)hk * G + g;
+        if (FA_IN_BOUNDS(p.status, row, (long)p.B * p.Hq)) {
+          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + row * D + idx % D) =
+              make_uint2(Elem<T>::pack(part.x, part.y), Elem<T>::pack(part.z, part.w));
+          if (idx % D == 0) p.lse[row] = lse;
+        }
       } else if (FA_IN_BOUNDS(p.status, slot, slots)) {
         *reinterpret_cast<float4*>(p.o_cache + slot * G * D + idx) = part;
         if (idx % D == 0) p.lse_cache[slot * G + g] = lse;
@@ -695,7 +705,7 @@ __global__ void __launch_bounds__(combine_threads(WARPS)) cache_combine_kernel(C
   const long row = (long)blockIdx.x * (kWarps / WARPS) + warp / WARPS;  // b Hq + h
   const long nrows = (long)p.B * p.Hq;
   if (WARPS == 1 && row >= nrows) return;
-  const bool any = row < nrows;  // (two warps a row: an odd number of rows leaves two without)
+  bool any = row < nrows;  // (two warps a row: an odd number of rows leaves two without)
   const int Sp = p.prefix_splits, G = p.Hq / p.Hkv;
   const int b = (int)(row / p.Hq), h = (int)(row - (long)b * p.Hq), hk = h / G;
   const bool has = any && p.seqlens[any ? b : 0] > 0;
@@ -703,6 +713,8 @@ __global__ void __launch_bounds__(combine_threads(WARPS)) cache_combine_kernel(C
   // came to lie unevenly on the SMs and cost 3 % of a long decode)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int2 span = has ? p.spans[b] : make_int2(0, -1);
+  if (Sp == 0 && G <= 8 && span.x == span.y) any = false;  // one CTA had it whole
+  if (WARPS == 1 && !any) return;
   const int live = any ? Sp + span.y - span.x + 1 : 0;
   const long slot0 = ((long)hk * (p.B + p.cache_ctas / p.Hkv) + b + span.x) * G + (h - hk * G);  // then G apart
   auto lse_of = [&](int s) { return s < Sp ? p.lse_part[row * Sp + s] : p.lse_cache[slot0 + (long)(s - Sp) * G]; };

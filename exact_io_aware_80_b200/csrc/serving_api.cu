@@ -50,10 +50,11 @@ fa_status check_decode(int B, int Hq, int Hkv, int Nk_max, int d, float scale, f
 }
 
 // CTAs of a cluster per sequence and KV head for a batch small enough to go without a separate merge
-// (0: too large): as many as 128 keys each leave, all resident at once (3 an SM), at most 1024 keys
-// each and 8 of a prefix's partials a row.
-int solo_of(int B, int Hkv, int Nk_max, int prefix_splits) {
-  const long long units = (long long)B * Hkv, most = 3 * 148;
+// (0: too large): as many as 128 keys each leave, all resident at once, at most 1024 keys each and 8 of a
+// prefix's partials a row.  64 sequences of up to 500 E4M3 keys, 8 KV heads of 64 (512 clusters of one, 740
+// resident): 9.3 us, with a merge of its own 13.2; heads of 128 (444 resident): 18.0 and 17.1.
+int solo_of(int B, int Hq, int Hkv, int Nk_max, int prefix_splits, int d, bool fp8) {
+  const long long units = (long long)B * Hkv, most = 148ll * fa::cache_ctas_per_sm(d, fp8, Hq / Hkv > 8);
   if (units > most || prefix_splits > 8) return 0;
   int n = 8;
   while (n > 1 && (units * n > most || 128ll * (n / 2) >= Nk_max)) n /= 2;
@@ -248,7 +249,7 @@ fa_status fa_fp8_cache_read(const void* k8, const void* v8, const float* k_scale
 
 size_t fa_decode_fp8_workspace_bytes(int B, int Hq, int Hkv, int Nk_max, int prefix_splits, int d) {
   if (B < 1 || Hq < 1 || Hkv < 1 || Nk_max < 1 || Hq % Hkv != 0 || prefix_splits < 0 || d < 1) return 0;
-  if (prefix_splits == 0 && solo_of(B, Hkv, Nk_max, 0) > 0) return 0;
+  if (prefix_splits == 0 && solo_of(B, Hq, Hkv, Nk_max, 0, d, true) > 0) return 0;
   return workspace_of(B, Hq, Hkv, prefix_splits, d).bytes;
 }
 
@@ -258,7 +259,7 @@ fa_status fa_decode_fp8(const void* q, const void* k8, const void* v8, const flo
   if (!q || !k8 || !v8 || !k_scale || !v_scale || !seqlens_k || !o || !lse) return FA_ERR_INVALID;
   const fa_status st = check_decode(B, Hq, Hkv, Nk_max, d, scale, dt);
   if (st != FA_OK) return st;
-  const int solo = solo_of(B, Hkv, Nk_max, 0);
+  const int solo = solo_of(B, Hq, Hkv, Nk_max, 0, d, true);
   if (!workspace && !solo) return FA_ERR_INVALID;
   if (!aligned(q, 16) || !aligned(k8, 16) || !aligned(v8, 16) || !aligned(o, 16) || !aligned(workspace, 16) ||
       !aligned(k_scale, 4) || !aligned(v_scale, 4) || !aligned(seqlens_k, 4) || !aligned(lse, 4))
@@ -351,7 +352,7 @@ fa_status fa_decode_shared_prefix(const void* q, const void* k_prefix, const voi
   a.prefix_splits = prefix_splits;
   a.after_prefix = 1;
   a.prefix_chunk = pchunk;
-  a.solo = solo_of(B, Hkv, Nk_max, prefix_splits);
+  a.solo = solo_of(B, Hq, Hkv, Nk_max, prefix_splits, d, k_scale != nullptr);
   const int sms = fa::device_sm_count();
   a.prefix_ctas = plan_prefix(B, Hq / Hkv, Hkv, Np, Nk_max, d, k_scale != nullptr, prefix_splits, sms).ctas;
   a.cache_ctas = cache_ctas_of(B, Hkv, Nk_max, d, Hq / Hkv, k_scale != nullptr, sms, a.prefix_ctas);

@@ -278,6 +278,12 @@ DECODE = [
     (2, 6, 3, 5000, 128, "bf16", [4999, 17]),
     (3, 4, 2, 8200, 64, "bf16", [0, 8200, 130]),
     (90, 10, 5, 140, 64, "fp16", [(37 * b) % 141 for b in range(90)]),
+    # more sequences and KV heads than resident clusters: several sequences to a CTA, whole or in part
+    (300, 6, 3, 40, 64, "bf16", [b % 41 for b in range(300)]),
+    (140, 5, 5, 300, 128, "fp16", [(61 * b) % 301 if b % 3 else 0 for b in range(140)]),
+    (400, 2, 2, 130, 64, "fp16", [(b * b) % 131 if b % 50 else 0 for b in range(400)]),
+    (57, 72, 8, 150, 128, "bf16", [(37 * b) % 151 for b in range(57)]),
+    (250, 2, 2, 700, 128, "bf16", [700 if b == 100 else (b * 7) % 130 for b in range(250)]),
 ]
 
 
