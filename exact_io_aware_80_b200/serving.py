@@ -19,26 +19,30 @@ from . import _lib
 __all__ = ["rotary_table", "rotary_magnitude", "rotary_fwd", "rotary_bwd", "fp8_cache_append", "fp8_cache_read",
            "decode_fp8", "decode_shared_prefix"]
 
-# These calls serve single tokens, where the host's share of a pass is the larger one; checks
-# therefore pass on one expression and take a bad tensor apart only to say what is wrong with it.
-_modules = None
+# These calls serve single tokens, where the host's share of a pass is the larger one: checks pass on
+# one expression and take a bad tensor apart only to say what is wrong with it, and what every call
+# looks up is looked up once.
+torch = None
+_entries: dict = {}
+_get_device = _get_stream = None
 
 
 def _torch():
-    global _modules
-    if _modules is None:
-        import torch
-        _modules = torch
-    return _modules
+    global torch, _get_device, _get_stream
+    if torch is None:
+        import torch as module
+        _get_device, _get_stream = module._C._cuda_getDevice, module._C._cuda_getCurrentRawStream
+        torch = module
+    return torch
 
 
 def _dt(t):
-    torch = _torch()
-    if t.dtype is torch.bfloat16:
+    dtype = t.dtype
+    if dtype is (torch or _torch()).bfloat16:
         return _lib.FA_BF16
-    if t.dtype is torch.float16:
+    if dtype is torch.float16:
         return _lib.FA_FP16
-    raise TypeError(f"attention tensors must be fp16 or bf16, got {t.dtype}")
+    raise TypeError(f"attention tensors must be fp16 or bf16, got {dtype}")
 
 
 def _device(t):
@@ -59,27 +63,25 @@ def _check(name, t, dtype, shape, dev, contiguous=True):
     raise ValueError(f"{name} must be contiguous")
 
 
-_entries: dict = {}
-
-
 def _call(dev, name, *args):
     """The C entry point with ``dev`` current, on its current stream."""
     fn = _entries.get(name)
     if fn is None:
         fn = _entries[name] = getattr(_lib.load(), name)
-    torch = _torch()
     index = dev.index
-    if index == torch._C._cuda_getDevice():
-        rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if index == _get_device():
+        rc = fn(*args, _get_stream(index))
     else:
         with torch.cuda.device(dev):
-            rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
-    if rc != _lib.FA_OK:
+            rc = fn(*args, _get_stream(index))
+    if rc != 0:  # FA_OK
         raise _lib.FAError(name, rc)
 
 
 def _strides(name, t, B, N, H, d):
     """(batch, token) strides of [B, N, H, d] whose heads are contiguous."""
+    if t.is_contiguous():
+        return N * H * d, H * d
     sb, sn, sh, sd = t.stride()
     if (sh != d and H > 1) or (sd != 1 and d > 1):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
@@ -136,14 +138,14 @@ def rotary_magnitude(factor: float) -> float:
 
 
 def _rotary(q, k, positions, table, interleaved, magnitude, inverse, q_out, k_out):
-    torch = _torch()
     dt, dev, dtype, shape = _dt(q), _device(q), q.dtype, q.shape
     B, N, Hq, d = shape
     each = positions.dim() == 2
     _check("positions", positions, torch.int32, (B, N) if each else (N,), dev)
     pairs = table.numel()
     _check("table", table, torch.int64, (pairs,), dev)
-    (q_bs, q_ts), k_bs, k_ts, Hkv, kp, kop = _strides("q", q, B, N, Hq, d), 0, 0, 0, 0, 0
+    q_bs, q_ts = _strides("q", q, B, N, Hq, d)
+    k_bs = k_ts = Hkv = kp = kop = 0
     if q_out is None:
         q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
     else:
@@ -159,7 +161,7 @@ def _rotary(q, k, positions, table, interleaved, magnitude, inverse, q_out, k_ou
             _check("k_out", k_out, dtype, shape, dev)
         kp, kop = k.data_ptr(), k_out.data_ptr()
     _call(dev, "fa_rotary", q.data_ptr(), kp, q_out.data_ptr(), kop, positions.data_ptr(), table.data_ptr(), B, N,
-          Hq, Hkv, d, 2 * pairs, int(interleaved), int(inverse), magnitude, q_bs, q_ts, k_bs, k_ts,
+          Hq, Hkv, d, 2 * pairs, bool(interleaved), inverse, magnitude, q_bs, q_ts, k_bs, k_ts,
           N if each else 0, dt)
     return q_out, k_out
 
@@ -185,14 +187,16 @@ def rotary_bwd(dq, dk, positions, table, interleaved: bool = False, magnitude: f
 # the E4M3 cache
 # ---------------------------------------------------------------------------
 def _check_cache(k8, v8, k_scale, v_scale, B, Hkv, d, dev):
-    torch = _torch()
     Nk_max = k8.shape[1]
-    shape = (B, Nk_max, Hkv, d)
-    _check("k8", k8, torch.uint8, shape, dev)
-    _check("v8", v8, torch.uint8, shape, dev)
-    shape = (B, Hkv, Nk_max)
-    _check("k_scale", k_scale, torch.float32, shape, dev)
-    _check("v_scale", v_scale, torch.float32, shape, dev)
+    u8, f32, codes, scales = torch.uint8, torch.float32, (B, Nk_max, Hkv, d), (B, Hkv, Nk_max)
+    if not (k8.dtype is u8 and v8.dtype is u8 and k_scale.dtype is f32 and v_scale.dtype is f32 and
+            k8.shape == codes and v8.shape == codes and k_scale.shape == scales and v_scale.shape == scales and
+            k8.device == dev and v8.device == dev and k_scale.device == dev and v_scale.device == dev and
+            k8.is_contiguous() and v8.is_contiguous() and k_scale.is_contiguous() and v_scale.is_contiguous()):
+        _check("k8", k8, u8, codes, dev)
+        _check("v8", v8, u8, codes, dev)
+        _check("k_scale", k_scale, f32, scales, dev)
+        _check("v_scale", v_scale, f32, scales, dev)
     return Nk_max
 
 
@@ -202,7 +206,6 @@ def fp8_cache_append(k, v, k8, v8, k_scale, v_scale, start, counts=None):
     ``counts``: int32 [B], rows that each sequence appends (None: all n).  Rows that fall outside the
     cache are dropped.  k and v may be slices of one packed projection (heads contiguous).
     """
-    torch = _torch()
     dt, dev = _dt(k), _device(k)
     B, n, Hkv, d = k.shape
     _check("v", v, k.dtype, k.shape, dev, contiguous=False)
@@ -218,7 +221,7 @@ def fp8_cache_append(k, v, k8, v8, k_scale, v_scale, start, counts=None):
 def fp8_cache_read(k8, v8, k_scale, v_scale, seqlens_k, Nk: int | None = None, dtype=None):
     """The first Nk rows (None: all) of an E4M3 cache as (k, v) [B, Nk, Hkv, d] in ``dtype`` (bf16 by
     default), rows past seqlens_k[b] zero, via ``fa_fp8_cache_read``."""
-    torch = _torch()
+    _torch()
     dev = _device(k8)
     B, Nk_max, Hkv, d = k8.shape
     _check_cache(k8, v8, k_scale, v_scale, B, Hkv, d, dev)
@@ -244,7 +247,6 @@ def _plan(device, B, Hq, Hkv, Np, Nk_max, d, fp8, prefix_splits):
 
 
 def _decode_buffers(q, seqlens_k, need, workspace, out, lse):
-    torch = _torch()
     dev, dtype = q.device, q.dtype
     B, _, Hq, d = q.shape
     shape = (B, 1, Hq, d)
@@ -291,7 +293,6 @@ def decode_shared_prefix(q, k_prefix, v_prefix, k_cache, v_cache, seqlens_k, k_s
     seqlens_k[b] rows (0 allowed) of its own cache, [B, Nk_max, Hkv, d] in q's type, or uint8 E4M3
     codes with ``k_scale`` and ``v_scale`` (``fa_decode_shared_prefix``).
     """
-    torch = _torch()
     dt, dev, dtype = _dt(q), _device(q), q.dtype
     B, _, Hq, d = q.shape
     _, Np, Hkv, _ = k_prefix.shape
