@@ -51,7 +51,8 @@ using namespace sm100;
 constexpr int kBM = 128;     // rows of a query tile (= TMEM lanes)
 constexpr int kBN = 128;     // keys per K/V tile
 constexpr int kStages = 2;   // K/V ring depth
-constexpr int kRestRows = 32;  // up to so many query rows of a KV head P is taken as two 16-bit values
+// Up to so many query rows of a KV head, or so many keys, P is taken as two 16-bit values.
+constexpr int kRestRows = 32, kRestKeys = 1024;
 // Register split with two query tiles: launched at 168 per thread (384 x 168 = 64512), the
 // load/MMA warpgroup drops to 104 and the softmax warpgroups rise to 200 (2 x 128 x 200 +
 // 128 x 104 = 64512).  One query tile (256 threads) needs no split.
@@ -539,8 +540,10 @@ cudaError_t launch_d(const CacheDecodeArgs& a, cudaStream_t s) {
   if (a.B > kBM / G) return launch<T, D, 2, false>(a, s);
   // Every sequence fits one query tile.  Rounding P to 16 bits costs an output as much as its own
   // rounding does: over many outputs 1.41 times the error of the last rounding alone, over the few of
-  // a small batch up to 1.6.  There P's rest is multiplied too (1.83 us a K/V tile instead of 1.57).
-  return a.B * G <= kRestRows ? launch<T, D, 1, true>(a, s) : launch<T, D, 1, false>(a, s);
+  // a small batch up to 1.6.  There P's rest is multiplied too (1.83 us a K/V tile instead of 1.57);
+  // and so it is behind a short prefix, where a call is mostly launches (32 sequences behind 1000 keys 15.1 us and
+  // 1.00 times the error of one rounding, without it 14.7 and 1.30).
+  return a.B * G <= kRestRows || a.Np <= kRestKeys ? launch<T, D, 1, true>(a, s) : launch<T, D, 1, false>(a, s);
 }
 
 template <typename T>
