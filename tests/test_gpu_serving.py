@@ -393,6 +393,21 @@ def test_decode_shared_prefix(fa, B, Hq, Hkv, Np, Nk, d, dt, fp8, ps):
                  max(F8_STEP, torch.finfo(DT[dt]).eps / 2), F8_FLOOR)
 
 
+# (q's type and size, scale): scale 0 weighs every key alike, keys past the prefix's end not at all
+@pytest.mark.parametrize("dt,size,scale", [("bf16", 1.0, 0.0), ("fp16", 1.0, 0.0), ("bf16", 1.0, 2.0),
+                                           ("fp16", 2000.0, 1e-4), ("bf16", 1e20, 1e-21), ("bf16", 1e-20, 1e19)])
+@pytest.mark.parametrize("Np", [1, 65, 128, 200, 300])
+@pytest.mark.parametrize("B", [3, 70])  # one query tile; two of them, the second row block's last one empty
+def test_decode_shared_prefix_query_sizes_and_scales(fa, B, Np, dt, size, scale):
+    Hq, Hkv, Nk, d = 4, 1, 5, 64
+    lens = [b % (Nk + 1) for b in range(B)]
+    _, args, k, v = prefix_case(fa, B, Hq, Hkv, Np, Nk, d, dt, False, lens, 57)
+    q = normal((B, 1, Hq, d), DT[dt], 58, size=size)
+    o, lse = fa.decode_shared_prefix(q.cuda(), *args[1:], scale=scale)
+    done(fa)
+    check_decode(q, k, v, [Np + n for n in lens], scale, o, lse, max(F8_STEP, torch.finfo(DT[dt]).eps / 2), F8_FLOOR)
+
+
 @pytest.mark.parametrize("B", [2, 40])
 def test_decode_shared_prefix_passes_on_nan(fa, B):
     """One bad key of the prefix, in every column of a tile's exponentials, makes its KV head's rows NaN
