@@ -59,6 +59,11 @@ constexpr int kRestRows = 32, kRestKeys = 1024;
 constexpr int kRegsSoftmax = 200;
 constexpr int kRegsControl = 104;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: rescale O when m grows by more than 2^8
+// fp16 weights are kept 2^7 larger (m lowered by 7): at most 2^15, normal down to 2^-21 of the reference,
+// and off by 2^-32 of it at most below.  Unlifted, a key 2^-25 below another counted in l and not in O: of
+// 20000 such keys behind one whose value was 0 nothing was left.
+template <typename T>
+constexpr float kLift = Elem<T>::kBf16 ? 0.f : 7.f;
 
 // 2^x for two values on the FMA and integer pipes, as exp2_fma2 (sm100.cuh) does it but by a
 // degree-5 minimax polynomial (gen_exp2_poly.py 5; relative error 2.4e-7 against the 7.5e-5 of degree
@@ -383,7 +388,7 @@ __global__ void __launch_bounds__(Smem<D, NT, REST>::kThreads, 1)
           const float corr = resc ? ex2(m_ref - mxs) : 1.f;
           if (resc) m_ref = mxs;
           l *= corr;
-          const float mu = (m_ref == -INFINITY) ? 0.f : m_ref;
+          const float mu = (m_ref == -INFINITY ? 0.f : m_ref) - kLift<T>;
           const float2 c2 = make_float2(c, c), nm2 = make_float2(-mu, -mu);
           float2 rs0 = make_float2(0.f, 0.f), rs1 = make_float2(0.f, 0.f);
 #pragma unroll
@@ -458,7 +463,7 @@ __global__ void __launch_bounds__(Smem<D, NT, REST>::kThreads, 1)
       if (rr < p.G * p.seqs && b < p.B) {
         const long li = ((long)b * p.Hq + x.hk * p.G + rr % p.G) * p.S + x.s;
         if (FA_IN_BOUNDS(p.status, li, (long)p.B * p.Hq * p.S))
-          p.lse_part[li] = ((m_ref == -INFINITY ? 0.f : m_ref) + log2f(l)) * kLn2;
+          p.lse_part[li] = ((m_ref == -INFINITY ? 0.f : m_ref) - kLift<T> + log2f(l)) * kLn2;
       }
       const uint32_t half = sb + L::kOffStage + t * L::kPanel;
 #pragma unroll

@@ -408,6 +408,26 @@ def test_decode_shared_prefix_query_sizes_and_scales(fa, B, Np, dt, size, scale)
     check_decode(q, k, v, [Np + n for n in lens], scale, o, lse, max(F8_STEP, torch.finfo(DT[dt]).eps / 2), F8_FLOOR)
 
 
+@pytest.mark.parametrize("B", [4, 40, 140])  # few rows; one query tile; two
+def test_decode_shared_prefix_keeps_a_long_faint_tail(fa, B):
+    """One dominant key whose value is 0 and 20000 keys 17.4 to 17.8 nats (25.1 to 25.7 powers of two) below
+    it, which together are all of O: 4e-4 of their values.  A weight is kept in fp16 in units in which the
+    largest is 2^7 to 2^15, so it is off by at most half of 2^-24 of that unit, 2^-32 of the largest."""
+    Np, d = 20001, 64
+    g = torch.Generator().manual_seed(59)
+    kp, vp = torch.zeros(1, Np, 1, d), 0.5 + torch.rand(1, Np, 1, d, generator=g)
+    kp[..., 0] = 2.2 + 0.4 * torch.rand(1, Np, 1, generator=g)
+    kp[0, 0, 0, 0], vp[0, 0] = 20.0, 0.0
+    q = torch.zeros(B, 1, 1, d)
+    q[..., 0] = 1.0
+    q, kp, vp = q.half(), kp.half(), vp.half()
+    own = torch.full((B, 1, 1, d), float("nan"), dtype=torch.float16).cuda()
+    o, lse = fa.decode_shared_prefix(q.cuda(), kp.cuda(), vp.cuda(), own, own, ints([0] * B), prefix_splits=1, scale=1.0)
+    done(fa)
+    assert torch.equal(o, o[:1].expand_as(o)) and torch.equal(lse, lse[:1].expand_as(lse))  # equal queries
+    check_decode(q[:1], f64(kp), f64(vp), [Np], 1.0, o[:1], lse[:1], F8_STEP, 2.0 ** -32)
+
+
 @pytest.mark.parametrize("B", [2, 40])
 def test_decode_shared_prefix_passes_on_nan(fa, B):
     """One bad key of the prefix, in every column of a tile's exponentials, makes its KV head's rows NaN
