@@ -243,7 +243,8 @@ def _plan(device, B, Hq, Hkv, Np, Nk_max, d, fp8, prefix_splits):
     if prefix_splits is None:
         with _torch().cuda.device(device):
             prefix_splits = _lib.fa_decode_prefix_splits(B, Hq, Hkv, Np, Nk_max, d, fp8)
-    return prefix_splits, _lib.fa_decode_fp8_workspace_bytes(B, Hq, Hkv, Nk_max, prefix_splits, d)
+    # (more splits than tiles are refused by the call itself, not for want of memory)
+    return prefix_splits, _lib.fa_decode_fp8_workspace_bytes(B, Hq, Hkv, Nk_max, min(prefix_splits, -(-Np // 128)), d)
 
 
 def _decode_buffers(q, seqlens_k, need, workspace, out, lse):
@@ -317,5 +318,5 @@ def decode_shared_prefix(q, k_prefix, v_prefix, k_cache, v_cache, seqlens_k, k_s
     workspace, out, lse = _decode_buffers(q, seqlens_k, need, workspace, out, lse)
     _call(dev, "fa_decode_shared_prefix", q.data_ptr(), k_prefix.data_ptr(), v_prefix.data_ptr(),
           k_cache.data_ptr(), v_cache.data_ptr(), ksp, vsp, seqlens_k.data_ptr(), out.data_ptr(), lse.data_ptr(),
-          workspace.data_ptr(), B, Hq, Hkv, Np, Nk_max, d, scale, prefix_splits, dt)
+          0 if workspace is None else workspace.data_ptr(), B, Hq, Hkv, Np, Nk_max, d, scale, prefix_splits, dt)
     return out, lse

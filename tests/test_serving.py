@@ -129,6 +129,40 @@ def test_python_calls_refuse_cpu_tensors_and_bad_metadata():
         fa.decode_shared_prefix(q[:, :1], q[:1], q[:1], q, q, lens)
 
 
+def test_python_decode_calls_leave_bad_sizes_to_the_library(lib, monkeypatch):
+    """Sizes for which no workspace is planned reach the C entry, whose refusal is the error raised (host
+    tensors in place of device ones: validation fails before any of them is touched)."""
+    torch = pytest.importorskip("torch")
+    import exact_io_aware_80_b200 as fa
+    from exact_io_aware_80_b200 import serving
+    serving._torch()
+    monkeypatch.setattr(serving, "_device", lambda t: t.device)
+    monkeypatch.setattr(serving, "_get_device", lambda: None)
+    monkeypatch.setattr(serving, "_get_stream", lambda index: None)
+
+    def refused(Hq=4, Hkv=2, Nk=64, Np=10, fp8=True, splits=1, prefix=True):
+        q, lens = torch.zeros(2, 1, Hq, 64, dtype=torch.float16), torch.zeros(2, dtype=torch.int32)
+        codes, scales = torch.zeros(2, Nk, Hkv, 64, dtype=torch.uint8), torch.ones(2, Hkv, Nk)
+        kp, own = torch.zeros(1, Np, Hkv, 64, dtype=torch.float16), torch.zeros(2, Nk, Hkv, 64, dtype=torch.float16)
+        with pytest.raises(fa.FAError):
+            if not prefix:
+                fa.decode_fp8(q, codes, codes, scales, scales, lens)
+            elif fp8:
+                fa.decode_shared_prefix(q, kp, kp, codes, codes, lens, scales, scales, prefix_splits=splits)
+            else:
+                fa.decode_shared_prefix(q, kp, kp, own, own, lens, prefix_splits=splits)
+
+    for fp8 in (True, False):
+        refused(Hq=5, fp8=fp8)
+        refused(Nk=0, fp8=fp8)
+        refused(Np=0, fp8=fp8)
+        for splits in (0, -1, 2, 1 << 30):  # the last: no workspace of 2 TB is asked for first
+            refused(fp8=fp8, splits=splits)
+        refused(Nk=9000, fp8=fp8, splits=0)
+    refused(Hq=5, prefix=False)
+    refused(Nk=0, prefix=False)
+
+
 def test_rotary_table_holds_turns_per_position():
     fa = pytest.importorskip("exact_io_aware_80_b200")
     for kw, ref in ((dict(), dict()), (dict(base=500000.0), dict(base=500000.0)),
