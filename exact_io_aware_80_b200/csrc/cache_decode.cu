@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, cache_ctas_per_sm(D, F8, NB == 2)) c
 
   // W, this CTA's part [begin, end) of the line, and the sequence that begin lies in.  Every warp for
   // itself: a lane sums the blocks of a stretch of sequences, and the one whose stretch holds begin walks it
-  auto length = [&](int b) { return min(max(p.seqlens[b], 0), p.Nk_max); };
+  auto length = [&](int b) { return FA_IN_BOUNDS(p.status, b, p.B) ? min(max(p.seqlens[b], 0), p.Nk_max) : 0; };
   auto blocks = [&](int n) { return (n + kBlock - 1) / kBlock; };
   int begin, end, W = 0, C = 0;  // W < 2^31: a block of a head takes 4 KB at least
   int cb = 0, cblk = 0, cn = 0, cpos;  // the cursor: block cblk of sequence cb, of cn keys, at place cpos
@@ -273,6 +273,16 @@ __global__ void __launch_bounds__(kThreads, cache_ctas_per_sm(D, F8, NB == 2)) c
   } src;
   src.left = 0;
   const long kstride = (long)kBlock * row_bytes;
+  // (of the checking build: 16 bytes of K and of V, and a key's two scales, lie inside the cache)
+  auto inside = [&](const uint8_t* k, const uint8_t* v) {
+    const long last = (long)p.B * p.Nk_max * row_bytes - 15;
+    return FA_IN_BOUNDS(p.status, k - static_cast<const uint8_t*>(p.k), last) &&
+           FA_IN_BOUNDS(p.status, v - static_cast<const uint8_t*>(p.v), last);
+  };
+  auto inside_scales = [&](const float* ks, const float* vs) {
+    const long all = (long)p.B * p.Hkv * p.Nk_max;
+    return FA_IN_BOUNDS(p.status, ks - p.k_scale, all) && FA_IN_BOUNDS(p.status, vs - p.v_scale, all);
+  };
   auto aim = [&](const Item& it) {
     const long row = ((long)it.b * p.Nk_max + it.first + lr) * p.Hkv + hk;
     src.k = static_cast<const uint8_t*>(p.k) + row * R::kRow + 16 * lc;
@@ -291,8 +301,10 @@ __global__ void __launch_bounds__(kThreads, cache_ctas_per_sm(D, F8, NB == 2)) c
       const uint8_t *pk = src.k, *pv = src.v;
 #pragma unroll
       for (int j = 0; j < R::kStep / kRows; ++j) {
-        cp_async16(st + chunk_at<R::kRow>(lr + j * kRows, lc), pk, true);
-        cp_async16(st + R::kTile + chunk_at<R::kRow>(lr + j * kRows, lc), pv, true);
+        if (inside(pk, pv)) {
+          cp_async16(st + chunk_at<R::kRow>(lr + j * kRows, lc), pk, true);
+          cp_async16(st + R::kTile + chunk_at<R::kRow>(lr + j * kRows, lc), pv, true);
+        }
         pk += kRows * row_bytes;
         pv += kRows * row_bytes;
       }
@@ -300,15 +312,15 @@ __global__ void __launch_bounds__(kThreads, cache_ctas_per_sm(D, F8, NB == 2)) c
 #pragma unroll 1
       for (int j = 0; j < R::kStep / kRows; ++j) {
         const int r = lr + j * kRows;
-        const bool ok = r < src.keys;
-        const long off = ok ? j * kRows * row_bytes : 0;
+        const long off = r < src.keys ? j * kRows * row_bytes : 0;
+        const bool ok = r < src.keys && inside(src.k + off, src.v + off);
         cp_async16(st + chunk_at<R::kRow>(r, lc), ok ? src.k + off : static_cast<const uint8_t*>(p.k), ok);
         cp_async16(st + R::kTile + chunk_at<R::kRow>(r, lc), ok ? src.v + off : static_cast<const uint8_t*>(p.v), ok);
       }
     }
     if constexpr (F8) {
       const int r = lane % R::kStep;
-      const bool ok = r < src.keys;
+      const bool ok = r < src.keys && inside_scales(src.ks, src.vs);
       cp_async4(st + 2 * R::kTile + 4 * r, ok ? src.ks : p.k_scale, ok);
       cp_async4(st + 2 * R::kTile + 4 * (R::kStep + r), ok ? src.vs : p.v_scale, ok);
       src.ks += kBlock;
@@ -330,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, cache_ctas_per_sm(D, F8, NB == 2)) c
 #pragma unroll
       for (int j = 0; j < D / 16; ++j) {
         qf[nb][j][0] = qf[nb][j][1] = 0u;
-        if (row < G) {
+        if (row < G && FA_IN_BOUNDS(p.status, (long)it.b * p.Hq + (long)hk * G + row, (long)p.B * p.Hq)) {
           const uint16_t* q0 = gq + (long)row * D + 16 * j;
           if constexpr (F8) {
             const uint2 w = *reinterpret_cast<const uint2*>(q0 + 4 * c);
@@ -708,7 +720,7 @@ __global__ void __launch_bounds__(combine_threads(WARPS)) cache_combine_kernel(C
   bool any = row < nrows;  // (two warps a row: an odd number of rows leaves two without)
   const int Sp = p.prefix_splits, G = p.Hq / p.Hkv;
   const int b = (int)(row / p.Hq), h = (int)(row - (long)b * p.Hq), hk = h / G;
-  const bool has = any && p.seqlens[any ? b : 0] > 0;
+  const bool has = any && FA_IN_BOUNDS(p.status, b, p.B) && p.seqlens[any ? b : 0] > 0;
   // (no early start for what follows: the next pass's CTAs, taking their places among this kernel's,
   // came to lie unevenly on the SMs and cost 3 % of a long decode)
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -717,6 +729,11 @@ __global__ void __launch_bounds__(combine_threads(WARPS)) cache_combine_kernel(C
   if (WARPS == 1 && !any) return;
   const int live = any ? Sp + span.y - span.x + 1 : 0;
   const long slot0 = ((long)hk * (p.B + p.cache_ctas / p.Hkv) + b + span.x) * G + (h - hk * G);  // then G apart
+  auto inside = [&](int s) {  // (of the checking build)
+    const long slots = (long)p.Hkv * (p.B + p.cache_ctas / p.Hkv);
+    return s < Sp ? FA_IN_BOUNDS(p.status, row * Sp + s, nrows * Sp)
+                  : FA_IN_BOUNDS(p.status, slot0 + (long)(s - Sp) * G, slots * G);
+  };
   auto lse_of = [&](int s) { return s < Sp ? p.lse_part[row * Sp + s] : p.lse_cache[slot0 + (long)(s - Sp) * G]; };
   auto load = [&](int s, float (&x)[kCols]) {
     const float* src =
@@ -740,7 +757,7 @@ __global__ void __launch_bounds__(combine_threads(WARPS)) cache_combine_kernel(C
     lse[i] = -INFINITY;
 #pragma unroll
     for (int c = 0; c < kCols; ++c) x[i][c] = 0.f;
-    if (s < live) {
+    if (s < live && inside(s)) {
       lse[i] = lse_of(s);
       load(s, x[i]);
     }
@@ -759,7 +776,7 @@ __global__ void __launch_bounds__(combine_threads(WARPS)) cache_combine_kernel(C
   };
 #pragma unroll
   for (int i = 0; i < kAhead; ++i) add(lse[i], x[i], mx == -INFINITY ? 0.f : mx);
-  for (int s = part + kAhead * WARPS; s < live; s += WARPS) {
+  for (int s = part + kAhead * WARPS; s < live && inside(s); s += WARPS) {
     const float v = lse_of(s);
     load(s, x[0]);
     if (v > mx) {

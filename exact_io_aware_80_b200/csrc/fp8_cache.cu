@@ -102,8 +102,9 @@ __global__ void __launch_bounds__(kThreads) append_kernel(Fp8CacheArgs p, Rows r
   uint4 w[TENSORS][2] = {};
   if (r < rows.count) {
     const Row at = row_at(rows, r);
-    const long dst = (long)p.start[at.b] + at.i;
-    if ((int)at.i < (p.counts ? p.counts[at.b] : p.n) && dst >= 0 && dst < p.Nk_max) {
+    const bool known = FA_IN_BOUNDS(p.status, at.b, p.B);
+    const long dst = known ? (long)p.start[at.b] + at.i : -1;
+    if (known && (int)at.i < (p.counts ? p.counts[at.b] : p.n) && dst >= 0 && dst < p.Nk_max) {
       const long c = ((long)at.b * p.Nk_max + dst) * p.Hkv + at.h;
       srow = ((long)at.b * p.Hkv + at.h) * p.Nk_max + dst;
       if (FA_IN_BOUNDS(p.status, c, (long)p.B * p.Nk_max * p.Hkv) &&
@@ -181,7 +182,7 @@ __global__ void __launch_bounds__(kThreads) read_kernel(Fp8CacheArgs p, Rows row
     live[k] = false;
     if (r < rows.count) {
       const Row at = row_at(rows, r);
-      if ((int)at.i < p.counts[at.b]) {
+      if (FA_IN_BOUNDS(p.status, at.b, p.B) && (int)at.i < p.counts[at.b]) {
         const long crow = ((long)at.b * p.Nk_max + at.i) * p.Hkv + at.h;
         const long srow = ((long)at.b * p.Hkv + at.h) * p.Nk_max + at.i;
         if (FA_IN_BOUNDS(p.status, crow, (long)p.B * p.Nk_max * p.Hkv) &&
@@ -196,7 +197,7 @@ __global__ void __launch_bounds__(kThreads) read_kernel(Fp8CacheArgs p, Rows row
 #pragma unroll
   for (int k = 0; k < ROWS; ++k) {
     const uint32_t r = r0 + k * kPer;
-    if (r < rows.count && FA_IN_BOUNDS(p.status, r, rows.count))
+    if (r < rows.count && FA_IN_BOUNDS(p.status, (long)r * D + 8 * unit + 7, (long)p.B * p.n * p.Hkv * D))
       reinterpret_cast<uint4*>(static_cast<uint16_t*>(isv ? p.v_out : p.k_out) + (long)r * D)[unit] =
           live[k] ? decode8<T>(c[k], s[k]) : make_uint4(0u, 0u, 0u, 0u);
   }

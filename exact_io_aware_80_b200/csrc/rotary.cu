@@ -44,6 +44,7 @@ struct Params {
   int per_y;  // heads per grid row
   long q_bs, q_ts, k_bs, k_ts, pos_stride;
   long q_len, k_len;  // elements from q (k) to the end of its last row
+  long pos_len;       // positions
   float mag, sign;
   int* status;
 };
@@ -144,7 +145,8 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(Params p) {
     }
     if (turned && !have) {  // while the first batch is in flight
       have = true;
-      const long long pos = p.positions[b * p.pos_stride + n];
+      const long at = b * p.pos_stride + n;
+      const long long pos = FA_IN_BOUNDS(p.status, at, p.pos_len) ? p.positions[at] : 0;
       auto angle = [&](int j, float* sine, float* cosine) {
         const unsigned long long phase = (unsigned long long)pos * p.turns[8 * unit + j];
         sincospif((float)(int)(phase >> 32) * 0x1p-31f, sine, cosine);  // half turns in [-1, 1]
@@ -195,7 +197,7 @@ cudaError_t launch_rotary(const RotaryArgs& a, cudaStream_t s) {
            static_cast<uint16_t*>(a.k_out), a.positions, a.turns, (uint32_t)a.B * a.N, FastDiv(a.N), a.Hq, a.Hkv, a.rot, 0,
            a.q_bs, a.q_ts, a.k_bs, a.k_ts, a.pos_stride,
            (a.B - 1) * a.q_bs + (a.N - 1) * a.q_ts + (long)a.Hq * a.d,
-           (a.B - 1) * a.k_bs + (a.N - 1) * a.k_ts + (long)a.Hkv * a.d, a.magnitude, a.inverse ? -1.f : 1.f, a.status};
+           (a.B - 1) * a.k_bs + (a.N - 1) * a.k_ts + (long)a.Hkv * a.d, (a.B - 1) * a.pos_stride + a.N, a.magnitude, a.inverse ? -1.f : 1.f, a.status};
   if (a.bf16) return a.d == 128 ? launch_d<__nv_bfloat16, 128>(a, p, s) : launch_d<__nv_bfloat16, 64>(a, p, s);
   return a.d == 128 ? launch_d<__half, 128>(a, p, s) : launch_d<__half, 64>(a, p, s);
 }
