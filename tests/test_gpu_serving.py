@@ -667,6 +667,87 @@ def test_calls_follow_earlier_and_precede_later_work(fa):
     done(fa)
 
 
+@pytest.mark.parametrize("B,fp8", [(4, True), (4, False), (90, True), (90, False)])  # a cluster a sequence; a merge of its own
+def test_decode_shared_prefix_right_behind_what_it_reads(fa, B, fp8):
+    """Rotation of q in place and the rewriting of cache rows that the call before has read, followed by the
+    call with nothing in between, equal the same steps with a wait after each, bit for bit."""
+    Hq, Hkv, N, Np, d, steps = 8, 2, 150, 300, 64, 40
+    table = fa.rotary_table(d)
+    kp, vp = (normal((1, Np, Hkv, d), torch.float16, 151 + i).cuda() for i in range(2))
+    q0 = normal((B, 1, Hq, d), torch.float16, 153).cuda()
+    rows = [normal((B, 1, Hkv, d), torch.float16, 154 + i, size=1.0 + i % 5).cuda() for i in range(2 * steps)]
+    at = [ints([(37 * i + 11 * b) % N for b in range(B)]) for i in range(steps)]
+    pos, lens = ints([[b] for b in range(B)]), ints([N - b % 3 for b in range(B)])
+
+    def chain(wait):
+        cache = empty_cache(B, N, Hkv, d)
+        for c, x in zip(cache, (0x38, 0x38, 0.01, 0.01)):
+            c.fill_(x)
+        plain = [torch.zeros(B, N, Hkv, d, dtype=torch.float16, device="cuda") for _ in range(2)]
+        q, outs = q0.clone(), []
+        torch.cuda.synchronize()
+        for i in range(steps):
+            fa.fp8_cache_append(rows[2 * i], rows[2 * i + 1], *cache, at[i])
+            if wait:
+                torch.cuda.synchronize()
+            if not fp8:  # the cache's values as a 16-bit cache
+                plain = fa.fp8_cache_read(*cache, lens, N, torch.float16)
+            fa.rotary_fwd(q, None, pos, table, q_out=q)
+            if wait:
+                torch.cuda.synchronize()
+            outs += fa.decode_shared_prefix(q, kp, vp, *((cache[0], cache[1], lens, cache[2], cache[3]) if fp8 else
+                                                         (*plain, lens)))
+            if wait:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return outs
+
+    ref = chain(True)
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(ref, chain(False)))
+    done(fa)
+
+
+def test_two_threads_on_two_streams(fa):
+    """Calls made at once by two threads, each on a stream and tensors of its own, equal those made alone."""
+    import threading
+    shapes = [(40, 8, 2, 300, 64, torch.float16), (6, 16, 2, 200, 128, torch.bfloat16)]
+    table = {d: fa.rotary_table(d) for d in (64, 128)}
+
+    def work(i, outs):
+        B, Hq, Hkv, N, d, dt = shapes[i]
+        with torch.cuda.stream(streams[i]):
+            q, kp, vp = (x.clone() for x in data[i][:3])
+            cache = [c.clone() for c in data[i][3]]
+            lens = data[i][4].clone()
+            for step in range(30):
+                qr, kr = fa.rotary_fwd(q, kp[:, step:step + 1].expand(B, 1, Hkv, d), (lens + 400).view(B, 1), table[d])
+                fa.fp8_cache_append(kr, kr, *cache, lens)
+                lens += 1
+                outs += fa.decode_shared_prefix(qr, kp, vp, cache[0], cache[1], lens, cache[2], cache[3])
+                outs += fa.decode_fp8(qr, *cache, lens)
+            streams[i].synchronize()
+
+    streams = [torch.cuda.Stream() for _ in shapes]
+    data = []
+    for i, (B, Hq, Hkv, N, d, dt) in enumerate(shapes):
+        lens = [(17 * b) % (N - 30) for b in range(B)]
+        data.append((normal((B, 1, Hq, d), dt, 161).cuda(), normal((1, 400, Hkv, d), dt, 162 + i).cuda(),
+                     normal((1, 400, Hkv, d), dt, 164 + i).cuda(), filled_cache(fa, B, N, Hkv, d, lens, 166 + i)[0], ints(lens)))
+    alone, both = [[], []], [[], []]
+    torch.cuda.synchronize()
+    for i in range(2):
+        work(i, alone[i])
+    threads = [threading.Thread(target=work, args=(i, both[i])) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    done(fa)
+    for a, b in zip(alone, both):
+        assert len(b) == 4 * 30 and all(torch.equal(x, y) for x, y in zip(a, b))
+
+
 class Guarded:
     """A tensor between two stretches of sentinel bytes."""
     PAD = 64 * 1024
