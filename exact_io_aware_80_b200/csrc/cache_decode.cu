@@ -54,8 +54,9 @@
 //  * the weights p_j s^v_j are fp16 in units of 2^(e - 8), where 2^e exceeds
 //    every s^v seen so far: at most 2^14 (p up to 2^6), relative error 2^-11
 //    down to 2^-22 of 2^e, absolute 2^-33 of it below.
-// Measured (bf16, 32 query and 8 KV heads of 128): 64 sequences of up to 32768 keys, 3.34 GB, 496 us
-// with the merge, 6.7 TB/s or 1.03 of a plain copy; one of 32768 18.2 us; 16 of up to 2000 15.3 us.
+// Measured (bf16, 32 query and 8 KV heads of 128), with the merge: 64 sequences of up to 32768 keys, 3.34 GB,
+// 496 to 504 us, 6.7 to 6.6 TB/s or 1.03 to 1.01 of a plain copy; in a CUDA graph one of 32768 18.2 us, 16 of
+// up to 2000 15.3 us.  With 9 to 16 query heads a KV head, heads of 128 spill up to 104 bytes a thread.
 //
 // l sums the unrounded p_j.  fp16 weights of a 16-bit cache are kept 2^8 larger
 // (m lowered by 8) for the same reason: at most 2^14, normal down to 2^-22.
@@ -75,8 +76,9 @@ constexpr float kStale = 6.f;  // log2 units that a score may exceed the referen
 // Rounding the weights to 16 bits costs an output as much as its own rounding does: over many outputs
 // 1.41 times the error of the last rounding alone, over the few of a small batch up to 1.6.  With REST
 // the rounding errors are multiplied too, and only the last rounding shows.  A 16-bit cache always takes
-// it (its loads hide it); an E4M3 cache with bf16 output never (its weights are rounded to fp16), with
-// fp16 output up to so many rows (32 sequences of 3000 keys, 16 heads, d = 64: 39.6 us with, 33.6 without).
+// it (its loads hide it); an E4M3 cache with bf16 output never (its weights are rounded to fp16: 64 sequences
+// of 32768 keys, 1.01 times the error of one rounding), with fp16 output up to so many rows (32 sequences of
+// 3000 keys, 16 heads, d = 64: 39.6 us with, 33.6 without).
 constexpr int kRestRows = 256;
 constexpr int kMinUnit = -112;  // smallest e of the weights' unit (all powers of two below stay normal)
 

@@ -13,8 +13,9 @@
 // exponentials beyond, when several row blocks read one tile from L2.
 //
 // Measured (bf16, 32 query and 8 KV heads of 128), the whole call with the sequences' own caches and the
-// merge: 64 sequences behind 32768 keys with up to 1024 of their own, 337 MB and 35 GFLOP, 63.5 us, 5.3
-// TB/s or 0.81 of a plain copy; 250 behind 8192 with up to 512 E4M3 ones, 240 MB and 35 GFLOP, 72.9 us.
+// merge, in a CUDA graph with pauses, below the power cap: 64 sequences behind 32768 keys with up to 1024 of
+// their own, 337 MB and 35 GFLOP, 63.5 us, 5.3 TB/s or 0.81 of a plain copy; 250 behind 8192 with up to 512
+// E4M3 ones, 240 MB and 35 GFLOP, 72.9 us.  One call after another for seconds, at the cap: 74 and 82 us.
 //
 // The machinery is the forward kernel's (fwd_sm100.cu): a persistent CTA per
 // SM; one or two 128-row query tiles; one thread issuing TMA loads of K and V
@@ -51,7 +52,8 @@ using namespace sm100;
 constexpr int kBM = 128;     // rows of a query tile (= TMEM lanes)
 constexpr int kBN = 128;     // keys per K/V tile
 constexpr int kStages = 2;   // K/V ring depth
-// Up to so many query rows of a KV head, or so many keys, P is taken as two 16-bit values.
+// With one query tile, up to so many query rows of a KV head, or so many keys, P is taken as two 16-bit
+// values (launch_d).  One pair of limits for both types and head sizes, each measured at a point or two.
 constexpr int kRestRows = 32, kRestKeys = 1024;
 // Register split with two query tiles: launched at 168 per thread (384 x 168 = 64512), the
 // load/MMA warpgroup drops to 104 and the softmax warpgroups rise to 200 (2 x 128 x 200 +
@@ -545,12 +547,15 @@ cudaError_t launch(const CacheDecodeArgs& a, cudaStream_t s) {
 template <typename T, int D>
 cudaError_t launch_d(const CacheDecodeArgs& a, cudaStream_t s) {
   const int G = a.Hq / a.Hkv;
+  // Rounding P to 16 bits costs an output as much as its own rounding does: over many outputs 1.41 times
+  // the error of the last rounding alone, over the few of a small batch up to 1.6.  Multiplying P's rest
+  // too takes that back and half as many products more.  Two query tiles, whose softmax spills for it with
+  // heads of 128, go without at any length (64 sequences behind 32768 bf16 keys: error 1.40 and 64 us, with the
+  // rest 1.00 and 79; 250 behind 8192: 1.16 and 76, 1.01 and 98).
   if (a.B > kBM / G) return launch<T, D, 2, false>(a, s);
-  // Every sequence fits one query tile.  Rounding P to 16 bits costs an output as much as its own
-  // rounding does: over many outputs 1.41 times the error of the last rounding alone, over the few of
-  // a small batch up to 1.6.  There P's rest is multiplied too (1.83 us a K/V tile instead of 1.57);
-  // and so it is behind a short prefix, where a call is mostly launches (32 sequences behind 1000 keys 15.1 us and
-  // 1.00 times the error of one rounding, without it 14.7 and 1.30).
+  // One tile takes it for the few rows of a small batch (1.83 us a K/V tile instead of 1.57) and behind a
+  // short prefix, where a call is mostly launches (32 sequences behind 1000 keys 15.1 us and 1.00 times the
+  // error of one rounding, without it 14.7 and 1.30).
   return a.B * G <= kRestRows || a.Np <= kRestKeys ? launch<T, D, 1, true>(a, s) : launch<T, D, 1, false>(a, s);
 }
 

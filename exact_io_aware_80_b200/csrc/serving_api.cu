@@ -52,7 +52,9 @@ fa_status check_decode(int B, int Hq, int Hkv, int Nk_max, int d, float scale, f
 // CTAs of a cluster per sequence and KV head for a batch small enough to go without a separate merge
 // (0: too large): as many as 128 keys each leave, all resident at once, at most 1024 keys each and 8 of a
 // prefix's partials a row.  64 sequences of up to 500 E4M3 keys, 8 KV heads of 64 (512 clusters of one, 740
-// resident): 9.3 us, with a merge of its own 13.2; heads of 128 (444 resident): 18.0 and 17.1.
+// resident): 9.3 us, with a merge of its own 13.2; heads of 128 (444 resident): 18.0 and 17.1.  Resident on the
+// 148 SMs of a B200, whatever device is current: the workspace, which a cluster does without, has to be the
+// same wherever its bytes are asked for.
 int solo_of(int B, int Hq, int Hkv, int Nk_max, int prefix_splits, int d, bool fp8) {
   const long long units = (long long)B * Hkv, most = 148ll * fa::cache_ctas_per_sm(d, fp8, Hq / Hkv > 8);
   if (units > most || prefix_splits > 8) return 0;
@@ -103,10 +105,12 @@ long long prefix_row_blocks(int B, int G) {
 
 // CTAs of the prefix kernel for a number of splits, and an estimate of the call's time in microseconds.
 // As measured: a K/V tile takes 2 with two query tiles, 1.6 with one, a work 4 more in its turn and the
-// kernel 5 to start and end; beside it an SM streams 60 KB of a 16-bit cache, 40 KB of an E4M3 one; four fifths
-// of a cache's room are taken to be in use.  The cache kernel fills the SMs that the prefix leaves, if they
-// are a quarter at least, or follows it, which costs 8 and a third of its time more.  64 sequences behind
-// 32768 keys, 1024 of their own: 80 CTAs 65 us, 144 79; 250 behind 8192, 512: 64 CTAs 73 us, 128 87.
+// kernel 5 to start and end (heads of 128; the same is taken for 64); beside it an SM streams 60 KB of a 16-bit
+// cache, 40 KB of an E4M3 one.  The lengths are on the device, so four fifths of a cache's room are taken to be
+// in use, and caches that hold far less leave the prefix too few SMs: 64 sequences of 100 E4M3 keys behind 8192
+// take 23 us in caches of 128 rows, 31 of 1024, 69 of 4096, 482 of 32768.  The cache kernel fills the SMs that the
+// prefix leaves, if they are a quarter at least, or follows it, which costs 8 and a third of its time more.  64
+// sequences behind 32768 keys, 1024 of their own: 80 CTAs 65 us, 144 79; 250 behind 8192, 512: 64 CTAs 73 us, 128 87.
 struct PrefixPlan {
   int ctas;
   double cost;

@@ -292,7 +292,8 @@ def decode_shared_prefix(q, k_prefix, v_prefix, k_cache, v_cache, seqlens_k, k_s
 
     Every sequence sees all of ``k_prefix``, ``v_prefix`` [1, Np, Hkv, d] and then the first
     seqlens_k[b] rows (0 allowed) of its own cache, [B, Nk_max, Hkv, d] in q's type, or uint8 E4M3
-    codes with ``k_scale`` and ``v_scale`` (``fa_decode_shared_prefix``).
+    codes with ``k_scale`` and ``v_scale`` (``fa_decode_shared_prefix``).  The GPU is divided between the
+    prefix and the caches by Nk_max: caches with far more room than their sequences use slow the call.
     """
     dt, dev, dtype = _dt(q), _device(q), q.dtype
     B, _, Hq, d = q.shape

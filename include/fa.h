@@ -451,6 +451,10 @@ int fa_decode_prefix_splits(int B, int Hq, int Hkv, int Np, int Nk_max, int d, i
  * fa_decode_fp8.  The prefix is cut into prefix_splits ranges of whole 128-key
  * tiles, none of them empty; workspace of
  * fa_decode_fp8_workspace_bytes(B, Hq, Hkv, Nk_max, prefix_splits, d) bytes.
+ * The SMs are divided between the prefix and the caches by Nk_max, since the
+ * lengths are on the device: caches that hold far less than Nk_max rows cost time
+ * as if they held four fifths of them.  Softmax weights are multiplied as 16-bit
+ * values; for few query rows or keys their rounding errors are multiplied too.
  */
 fa_status fa_decode_shared_prefix(const void* q, const void* k_prefix, const void* v_prefix, const void* k_cache,
                                   const void* v_cache, const float* k_scale, const float* v_scale,
